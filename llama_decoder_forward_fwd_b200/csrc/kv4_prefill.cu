@@ -58,11 +58,21 @@ DEVI float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-DEVI float max3(float a, float b, float c) {
+// Maxima that a NaN does not drop out of.
+DEVI float max2(float a, float b) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
+DEVI float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// A row's running maximum as it is kept. A NaN or infinite score makes the row NaN by its definition, but a
+// quarter of the exponentials (ex2_fma) lose a NaN: so the maximum carries it, to the row's sum and to all its weights.
+// An infinite maximum becomes NaN here, a finite one stays (x * 0 + x).
+DEVI float kept_max(float x) { return fmaf(x, 0.f, x); }
 // 2^x of a pair on the FMA pipe, for a share of the exponentials: x = n + f, n to the
 // exponent field, 2^f by a cubic with relative error below 1.5e-4, far below the bf16
 // rounding that P gets next.
@@ -684,11 +694,11 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
                 float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int i = 4; i < 64; i += 2) mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], s[i], s[i + 1]);
-                const float mine = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * sl2;
+                const float mine = max3(mx4[0], mx4[1], max2(mx4[2], mx4[3])) * sl2;
                 red_max[sb][half][r] = mine;
                 named_bar_sync(1 + q4, 64);
                 const float m_new = max3(m_used, mine, red_max[sb][half ^ 1][r]);
-                const bool need = m_new > m_used + KP_RESCALE_LOG2;  // false while the row has seen no key
+                const bool need = !(m_new <= m_used + KP_RESCALE_LOG2);  // false while the row has seen no key; true for NaN
                 const float alpha = need ? ex2(m_used - m_new) : 1.f;
                 // P buffer sb is free once PV of running tile gg-2 has completed
                 if (gg >= 2 && ok && !wait_for(&pv_done[sb], ((gg - 2) >> 1) & 1, err, DERR_ATTN_SOFTMAX_WAIT)) ok = false;
@@ -714,7 +724,7 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
                 }
                 if (need) {
                     l *= alpha;
-                    m_used = m_new;
+                    m_used = kept_max(m_new);
                 }
                 const float muse = m_used == -INFINITY ? 0.f : m_used;
                 const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(-muse, -muse);
@@ -1023,13 +1033,13 @@ template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_k
                 }
                 float mx[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(f(e), f(4 + e));
+                for (int e = 0; e < 4; ++e) mx[e] = max2(f(e), f(4 + e));
 #pragma unroll
                 for (int i = 8; i < 128; i += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], f(i + e), f(i + 4 + e));
-                const float m_new = fmaxf(m_used, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2);
-                const bool need = m_new > m_used + KP_RESCALE_LOG2;  // false while the row has seen no key
+                const float m_new = max2(m_used, max3(mx[0], mx[1], max2(mx[2], mx[3])) * sl2);
+                const bool need = !(m_new <= m_used + KP_RESCALE_LOG2);  // false while the row has seen no key; true for NaN
                 if (j > 0 && __any_sync(0xffffffffu, need)) {
                     // P V of the tile before is complete: the scores were issued after it
                     const float alpha = need ? ex2(m_used - m_new) : 1.f;
@@ -1050,7 +1060,7 @@ template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_k
                     }
                     tc_wait_st();
                 }
-                if (need) m_used = m_new;
+                if (need) m_used = kept_max(m_new);
                 const float muse = m_used == -INFINITY ? 0.f : m_used;
                 const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(-muse, -muse);
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

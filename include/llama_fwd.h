@@ -385,10 +385,11 @@ int llm_op_attention_decode_static(const void* q, const void* kcache, const void
  * bf16(scale * c + zero), rounded once. head_dim d is 64 or 128. A sequence's
  * block table lists its pages; a token's slot is page * page_size + its place in the
  * page (64-bit, as are all offsets derived from it).
- * Attention reads the values to the last bit where scales are below 2^66 and values
- * above 2^-54 (smaller ones to within 2^-62). Indices from run-time data (slots,
- * positions, table entries, lengths) are checked in both builds of the library; what
- * each call does with one out of range is said below, and none reports an error.
+ * Attention reads the values to the last bit where scales are below 2^67 (a group
+ * with a larger one reads as NaN) and values above 2^-54 (smaller ones to within
+ * 2^-62). Indices from run-time data (slots, positions, table entries, lengths) are
+ * checked in both builds of the library; what each call does with one out of range is
+ * said below, and none reports an error.
  * The calls use no memory but their operands, may be captured into CUDA graphs, and
  * calls on different streams may run at once as long as they share no buffer that
  * one of them writes (workspaces included). The current device must be the one that

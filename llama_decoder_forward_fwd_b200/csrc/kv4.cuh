@@ -37,7 +37,8 @@ __host__ __device__ constexpr int kv4_page_log2(int P) {
 // range of 256 steps, so its bits are 16 c * 2^-133. 2^133 is out of bf16's range: what comes
 // out is the value * 2^-72 (scale * 2^61, or * 2^57 for the upper half, zero * 2^-72), the same
 // rounding, and the products' results are scaled back in fp32. That holds for scales below
-// 2^66 and, to the last bit, for values above 2^-54 (smaller ones are off by up to 2^-62).
+// 2^67 (a group of a larger one reads as NaN) and, to the last bit, for values above 2^-54 (smaller ones
+// are off by up to 2^-62).
 constexpr float KV4_BACK = 4722366482869645213696.f;  // 2^72
 DEVI uint32_t kv4_mul(uint32_t a, uint32_t b) {
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -45,6 +46,8 @@ DEVI uint32_t kv4_mul(uint32_t a, uint32_t b) {
 }
 // A (scale, zero) pair times (2^61, 2^-72), as kv4_expand takes its parts; and a pair of such scales / 16.
 DEVI uint32_t kv4_pair(uint32_t sz) { return kv4_mul(sz, 0x1B805E00u); }
+// Whether a pair from kv4_pair holds an infinity or a NaN (a scale of 2^67 or more has become infinite).
+DEVI bool kv4_odd(uint32_t sz) { return (sz & 0x7F80u) == 0x7F80u || (sz & 0x7F800000u) == 0x7F800000u; }
 DEVI uint32_t kv4_16th(uint32_t s2) { return kv4_mul(s2, 0x3D803D80u); }
 // The eight codes of a word as four bf16 pairs, (value i, value i + 4) for i = 0..3, * 2^-72.
 DEVI void kv4_expand(uint32_t w, uint32_t s2, uint32_t s2_16th, uint32_t z2, uint32_t (&r)[4]) {

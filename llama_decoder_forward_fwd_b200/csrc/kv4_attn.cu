@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (kb + (ve ^ (j & 1)) + (j >> 1) * 8 >= s.len) vp[j] = 0;
-                            const bool bad = (vp[j] & 0x7F80u) == 0x7F80u || (vp[j] & 0x7F800000u) == 0x7F800000u;
+                            const bool bad = kv4_odd(vp[j]);
                             odd = odd || bad;
                             if (bad != second) vp[j] = 0;
                             else if (bad) vp[j] = 0x7F000000u;

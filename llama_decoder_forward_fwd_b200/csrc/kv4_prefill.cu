@@ -75,7 +75,7 @@ DEVI float max3(float a, float b, float c) {
 DEVI float kept_max(float x) { return fmaf(x, 0.f, x); }
 // 2^x of a pair on the FMA pipe, for a share of the exponentials: x = n + f, n to the
 // exponent field, 2^f by a cubic with relative error below 1.5e-4, far below the bf16
-// rounding that P gets next.
+// rounding that P gets next. -inf gives the clamp, just under 2^-126, and not 0 (see less_clamp).
 DEVI float2 ex2_fma(float2 x) {
     x.x = fmaxf(x.x, -126.f);
     x.y = fmaxf(x.y, -126.f);
@@ -87,6 +87,13 @@ DEVI float2 ex2_fma(float2 x) {
     p = __ffma2_rn(p, f, make_float2(0.99992806f, 0.99992806f));
     return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
                        __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+// A pair of weights from ex2_fma, in bf16, less 2^-126, which the clamp has become: a masked key's weight is 0 then,
+// however large its value is, and other weights change by nothing that a sum could show.
+DEVI uint32_t less_clamp(uint32_t w) {
+    const uint32_t least = 0x80808080u;
+    const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&least));
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 // mbar_wait whose polls may sleep in the barrier unit: the waiting warps' polls would otherwise take
 // issue slots from the softmax and the expansion.
@@ -363,11 +370,11 @@ template <int D> __global__ void __launch_bounds__(256) kv4_expand_kernel(const 
                 }
                 q = *reinterpret_cast<const uint32_t*>(src + 2 * rec.codes + (is_v ? rec.pairs : 0) + off * (D / 8) + t * (D / 4) / KV4_GROUP * 4);
             }
-            if ((q & 0x7F80u) == 0x7F80u || (q & 0x7F800000u) == 0x7F800000u) {
+            q = kv4_pair(q);
+            if (kv4_odd(q)) {
                 odd = true;
                 q = 0;
             }
-            q = kv4_pair(q);
             const uint32_t s2 = __byte_perm(q, 0, 0x1010), z2 = __byte_perm(q, 0, 0x3232), s2h = kv4_16th(s2);
 #pragma unroll
             for (int x = 0; x < WPL; ++x) {
@@ -535,12 +542,11 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
         auto store = [&](uint8_t* tile, const uint32_t (&c)[4][WPL], const uint32_t (&pr)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t q = pr[i];
-                if ((q & 0x7F80u) == 0x7F80u || (q & 0x7F800000u) == 0x7F800000u) {
+                uint32_t q = kv4_pair(pr[i]);
+                if (kv4_odd(q)) {
                     odd = true;
                     q = 0;
                 }
-                q = kv4_pair(q);
                 const uint32_t s2 = __byte_perm(q, 0, 0x1010), z2 = __byte_perm(q, 0, 0x3232), s2h = kv4_16th(s2);
                 const int r = i * 32 + key_l;
 #pragma unroll
@@ -740,7 +746,10 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
                         sum2[e & 1] = __fadd2_rn(sum2[e & 1], p[e]);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) pw[c * 4 + e] = pack_bf16x2(p[e].x, p[e].y);
+                    for (int e = 0; e < 4; ++e) {
+                        pw[c * 4 + e] = pack_bf16x2(p[e].x, p[e].y);
+                        if (e == 3) pw[c * 4 + e] = less_clamp(pw[c * 4 + e]);
+                    }
                 }
                 l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
                 tc_st_32x32b_x32(lane_base + KP_TMEM_P + sb * 64 + half * 32, pw);
@@ -762,7 +771,7 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
             lsum[half * KP_ROWS + r] = l;
             named_bar_sync(1 + q4, 64);
             l += lsum[(half ^ 1) * KP_ROWS + r];
-            // a row that saw no key: 0 (its clamped exponentials left a sum behind)
+            // a row that saw no key: 0
             const float inv = m_used != -INFINITY ? KV4_BACK / l : 0.f;
             __nv_bfloat16* dst = a.out + ((long long)(it.q0 + t) * a.H + h) * D + half * DPH;
             const long long prow_at = ((long long)blockIdx.x * 2 + (it.tile0 ? 0 : 1)) * KP_ROWS + r;  // of a part's result
@@ -1071,9 +1080,10 @@ template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_k
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float2 y = __ffma2_rn(make_float2(f(c * 32 + 2 * e), f(c * 32 + 2 * e + 1)), sl2x2, nmx2);
-                        const float2 p = (e & 3) < 3 ? make_float2(ex2(y.x), ex2(y.y)) : ex2_fma(y);  // a quarter on the FMA pipe  // a quarter on the FMA pipe
+                        const float2 p = (e & 3) < 3 ? make_float2(ex2(y.x), ex2(y.y)) : ex2_fma(y);  // a quarter on the FMA pipe
                         sum2[e & 1] = __fadd2_rn(sum2[e & 1], p);
                         pw[e] = pack_bf16x2(p.x, p.y);
+                        if ((e & 3) == 3) pw[e] = less_clamp(pw[e]);
                     }
                     tc_st_x16(S + c * 16, pw);
                     if (c == 1) {
@@ -1095,7 +1105,7 @@ template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_k
             g += it.nkt;
             if (ok && !wait_for(&pv_done[x], (g - 1) & 1, err, DERR_ATTN_SOFTMAX_WAIT)) ok = false;
             tc_fence_after();
-            // a row that saw no key: 0 (its clamped exponentials left a sum behind)
+            // a row that saw no key: 0
             const float inv = m_used != -INFINITY ? KV4_BACK / l : 0.f;
             __nv_bfloat16* dst = a.out + ((long long)(it.q0 + t) * a.H + h) * D;
             const long long slot = (long long)blockIdx.x * 2 + (it.tile0 ? 0 : 1);  // of a part's result

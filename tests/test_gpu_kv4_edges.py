@@ -89,3 +89,22 @@ def test_one_score_that_is_not_finite_gives_nan(lib, form, odd_score):
         got = case.run(L, mx)
         assert np.isnan(got[0, 1]).all(), at
         case.check(got, rows=lambda b: np.arange(max(0, at + 1 - (lens[b] - new[b])), new[b]))
+
+
+@pytest.mark.parametrize("top", [2.0**124, 1e30])
+@pytest.mark.parametrize("form", FORMS)
+def test_large_finite_values_behind_the_mask_leave_no_trace(lib, form, top):
+    """The last new tokens' values are huge: constant groups of 2^124, and groups whose scale passes 2^67. Rows before
+    them do not see them."""
+    import llama_decoder_forward_fwd_b200 as L
+    lens, new, H, Hk, d, P, mx = FORMS[form]
+    first = [l - max(1, min(40, n // 2)) if n > 1 else l for l, n in zip(lens, new)]  # the first huge key
+
+    def make(b, which, r):
+        if which == 0:
+            return None
+        x = r.randn(lens[b], Hk, d).astype(np.float32)
+        x[first[b]:] = top if top > 1e31 else top * np.arange(1, d + 1, dtype=np.float32)
+        return x
+    case = Case(lens, new, H, Hk, d, P, 8, make=make)
+    case.check(case.run(L, mx), rows=lambda b: np.arange(max(0, new[b] - (lens[b] - first[b]))))

@@ -151,7 +151,7 @@ struct llm_model {
     int kv_blocks = 0, kv_pages = 0;  // per sequence, of a layer's pool
     size_t kv_layer_bytes = 0, kv_ws_bytes = 0;
     uint8_t* kv_pool = nullptr;
-    int32_t *kv_table = nullptr, *kv_free = nullptr, *kv_used = nullptr;  // kv_used: before and after a step
+    int32_t *kv_table = nullptr, *kv_free = nullptr;
     int32_t *kv_q_start = nullptr, *kv_pos = nullptr, *kv_lens = nullptr;
     int64_t* kv_slots = nullptr;
     void* kv_ws = nullptr;
@@ -353,11 +353,11 @@ Epi base_epi(llm_model* m, int M, int T) {
 constexpr int kKv4Page = 64;  // tokens of a page of the model's own 4-bit cache
 
 // The plan of a step of T tokens per sequence over the 4-bit cache, shared by its layers: pages from the
-// pool's list in order (there are enough for every sequence at max_seq_len), slots and positions.
+// pool's list in order (there are enough for every sequence at max_seq_len), slots and positions. Which pages
+// are taken follows from the lengths alone, so that a step that fails after its plan takes none.
 int kv4_plan(llm_model* m, int B, int T) {
-    CK(launch_kv_pages(m->seq_len, nullptr, T, B, kKv4Page, m->kv_free, m->kv_pages, m->kv_used, m->kv_table, m->kv_blocks,
-                       m->kv_q_start, m->kv_pos, m->kv_slots, B * T, m->kv_lens, m->kv_used + 1, m->stream));
-    CK(cudaMemcpyAsync(m->kv_used, m->kv_used + 1, 4, cudaMemcpyDeviceToDevice, m->stream));
+    CK(launch_kv_pages(m->seq_len, nullptr, T, m->cfg.max_batch, B, kKv4Page, m->kv_free, m->kv_pages, nullptr, m->kv_table,
+                       m->kv_blocks, m->kv_q_start, m->kv_pos, m->kv_slots, B * T, m->kv_lens, nullptr, m->stream));
     return LLM_OK;
 }
 
@@ -608,7 +608,8 @@ int check_batch(llm_model* m, int B, int T) {
         if (m->host_len[b] + T > m->cfg.max_seq_len)
             return fail(LLM_ERR_SEQ_OVERFLOW, "sequence %d: length %d + %d > max_seq_len %d", b, m->host_len[b], T,
                         m->cfg.max_seq_len);
-    return LLM_OK;
+    // before anything is enqueued
+    return m->kv4 ? kv4_check_size(B, B * T, m->cfg.n_heads, m->cfg.n_kv_heads, m->kv_blocks, kKv4Page) : LLM_OK;
 }
 
 int max_keys_after(const llm_model* m, int B, int T) {
@@ -837,7 +838,6 @@ int llm_model_init(const llm_config* cfg, const llm_weights* w, void* stream, ll
         MALLOC_OR_BAIL(m->kv_pool, c.n_layers * m->kv_layer_bytes);
         MALLOC_OR_BAIL(m->kv_table, (size_t)m->kv_pages * 4);
         MALLOC_OR_BAIL(m->kv_free, (size_t)m->kv_pages * 4);
-        MALLOC_OR_BAIL(m->kv_used, 2 * 4);
         MALLOC_OR_BAIL(m->kv_q_start, (size_t)(c.max_batch + 1) * 4);
         MALLOC_OR_BAIL(m->kv_pos, Mx * 4);
         MALLOC_OR_BAIL(m->kv_lens, (size_t)c.max_batch * 4);
@@ -846,7 +846,6 @@ int llm_model_init(const llm_config* cfg, const llm_weights* w, void* stream, ll
         std::vector<int32_t> ids(m->kv_pages);
         for (int i = 0; i < m->kv_pages; ++i) ids[i] = i;
         if (cudaMemcpyAsync(m->kv_free, ids.data(), ids.size() * 4, cudaMemcpyHostToDevice, m->stream) != cudaSuccess ||
-            cudaMemsetAsync(m->kv_used, 0, 2 * 4, m->stream) != cudaSuccess ||
             cudaMemsetAsync(m->kv_table, 0xFF, (size_t)m->kv_pages * 4, m->stream) != cudaSuccess)
             return bail(fail(LLM_ERR_CUDA, "4-bit cache setup failed"));
     }
@@ -1130,7 +1129,6 @@ int llm_decode_step_hidden(llm_model* m, int B, const float* h_in, float* h_out)
 int llm_kv_cache_reset(llm_model* m) {
     if (!m) return fail(LLM_ERR_NULL_PTR, "model is NULL");
     CK(cudaMemsetAsync(m->seq_len, 0, (size_t)m->cfg.max_batch * 4, m->stream));
-    if (m->kv4) CK(cudaMemsetAsync(m->kv_used, 0, 4, m->stream));  // every page is free again
     for (auto& x : m->host_len) x = 0;
     return LLM_OK;
 }

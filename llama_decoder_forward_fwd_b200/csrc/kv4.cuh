@@ -61,8 +61,9 @@ DEVI void kv4_expand(uint32_t w, uint32_t s2, uint32_t s2_16th, uint32_t z2, uin
 }
 
 // ---- what the model's own path uses ----
-// llm_op_kv_pages; n_new null: n_each new tokens for every sequence.
-cudaError_t launch_kv_pages(const int32_t* lens, const int32_t* n_new, int n_each, int B, int page_size,
+// llm_op_kv_pages; n_new null: n_each new tokens for every sequence; held > 0: the pages taken already are
+// those of the first `held` lengths, whatever became of earlier plans (used_in and used_out null).
+cudaError_t launch_kv_pages(const int32_t* lens, const int32_t* n_new, int n_each, int held, int B, int page_size,
                             const int32_t* free_pages, int n_free, const int32_t* used_in, int32_t* table, int max_blocks,
                             int32_t* q_start, int32_t* positions, int64_t* slots, int N, int32_t* new_lens,
                             int32_t* used_out, cudaStream_t s);
@@ -78,6 +79,8 @@ struct Kv4StoreArgs {
     int lp;
 };
 cudaError_t launch_kv4_store(const Kv4StoreArgs& a, int d, cudaStream_t s);
+// LLM_OK, or why a call of these sizes is more than llm_op_attention_kv4 takes.
+int kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size);
 // llm_op_attention_kv4 with the error word of the caller's model.
 int attention_kv4(const void* q, const void* pool, int n_pages, int page_size, const int32_t* table, int max_blocks,
                   const int32_t* lens, const int32_t* q_start, int B, int N, int max_new, int H, int Hk, int d, void* out,

@@ -819,6 +819,14 @@ extern "C" int llm_op_attention_kv4(const void* q, const void* pool, int n_pages
                          workspace, workspace_bytes, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int lfw::kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size) {
+    // units are counted in 32 bits, and a row is divided by G as 32-bit fixed point
+    const long long G = H / Hk, chunks = (long long)N * G / 8 + B, tiles = ((long long)max_blocks * page_size + 31) / 32;
+    if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > (1LL << 31) / tiles)
+        return set_error(LLM_ERR_UNSUPPORTED, "more query rows or keys than one call takes");
+    return LLM_OK;
+}
+
 int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_size, const int32_t* table, int max_blocks,
                        const int32_t* lens, const int32_t* q_start, int B, int N, int max_new, int H, int Hk, int d,
                        void* out, void* workspace, size_t workspace_bytes, uint32_t* err, cudaStream_t s) {
@@ -828,12 +836,7 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
     if (!q || !pool || !table || !lens || !q_start || !out || !workspace)
         return set_error(LLM_ERR_NULL_PTR, "NULL operand or workspace");
     if (n_pages < 0) return set_error(LLM_ERR_BAD_ARG, "n_pages must not be negative");
-    {
-        // units are counted in 32 bits, and a row is divided by G as 32-bit fixed point
-        const long long G = H / Hk, chunks = (long long)N * G / 8 + B, tiles = ((long long)max_blocks * page_size + 31) / 32;
-        if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > (1LL << 31) / tiles)
-            return set_error(LLM_ERR_UNSUPPORTED, "more query rows or keys than one call takes");
-    }
+    if (const int too_large = kv4_check_size(B, N, H, Hk, max_blocks, page_size)) return too_large;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(pool) | reinterpret_cast<uintptr_t>(out) |
          reinterpret_cast<uintptr_t>(workspace)) & 15)
         return set_error(LLM_ERR_BAD_ARG, "operands must be 16-byte aligned");

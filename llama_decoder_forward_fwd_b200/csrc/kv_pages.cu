@@ -29,6 +29,7 @@ struct PagesArgs {
     int64_t* slots;
     int B, lp, n_free, max_blocks, N;
     int n_each;  // new tokens of every sequence when n_new is null
+    int held;    // sequences of lens, B or more, whose pages are the ones taken already; used_in is null then
 };
 
 DEVI int sat32(long long v) { return v > 0x7fffffffLL ? 0x7fffffff : (int)v; }
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(PG_THREADS) kv_pages_kernel(const PagesArgs a)
     pdl_wait();
     pdl_trigger();
     long long rows = 0, pages = a.used_in ? (long long)*a.used_in : 0;
+    for (int i = 0; i < a.held; ++i) pages += ((long long)max(a.lens[i], 0) + P - 1) >> a.lp;
     for (int c = 0, it = 0; c < a.B; c += PG_THREADS, ++it) {
         const int buf = it & 1, b = c + tid;
         long long len = 0, n = 0;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(PG_THREADS) kv_pages_kernel(const PagesArgs a)
     }
     if (blockIdx.x == 0 && tid == 0) {
         a.q_start[a.B] = sat32(rows);
-        *a.used_out = sat32(pages);
+        if (a.used_out) *a.used_out = sat32(pages);
     }
 }
 
@@ -162,17 +164,17 @@ extern "C" int llm_op_kv_pages(const int32_t* lens, const int32_t* n_new, int B,
         for (const auto& o : out)
             if (i.n && o.n && overlap(i.p, i.n, o.p, o.n))
                 return set_error(LLM_ERR_BAD_ARG, "an output overlaps an input (lens, n_new, free_pages, used_in)");
-    const cudaError_t e = lfw::launch_kv_pages(lens, n_new, 0, B, page_size, free_pages, n_free, used_in, table, max_blocks, q_start,
+    const cudaError_t e = lfw::launch_kv_pages(lens, n_new, 0, 0, B, page_size, free_pages, n_free, used_in, table, max_blocks, q_start,
                                                positions, slots, N, new_lens, used_out, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LLM_OK : set_error(LLM_ERR_CUDA, cudaGetErrorString(e));
 }
 
-cudaError_t lfw::launch_kv_pages(const int32_t* lens, const int32_t* n_new, int n_each, int B, int page_size,
+cudaError_t lfw::launch_kv_pages(const int32_t* lens, const int32_t* n_new, int n_each, int held, int B, int page_size,
                                  const int32_t* free_pages, int n_free, const int32_t* used_in, int32_t* table,
                                  int max_blocks, int32_t* q_start, int32_t* positions, int64_t* slots, int N,
                                  int32_t* new_lens, int32_t* used_out, cudaStream_t s) {
     PagesArgs a{lens, n_new, free_pages, used_in, table, q_start, positions, new_lens, used_out, slots, B,
-                kv4_page_log2(page_size), n_free, max_blocks, N, n_each};
+                kv4_page_log2(page_size), n_free, max_blocks, N, n_each, held};
     // one CTA per 256 token rows, at most one per SM: a CTA more repeats the scan
     const int sms = current_num_sms();
     int grid = (N + PG_THREADS - 1) / PG_THREADS;

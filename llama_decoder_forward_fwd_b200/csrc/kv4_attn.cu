@@ -142,16 +142,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     constexpr int VW = D / 64;   // and per key of V
     constexpr int MT = D / 16;   // 16-row tiles of O^T
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int wsum[W];
+    __shared__ long long wsum[W];
     constexpr int WL = W > 16 ? 32 : W > 8 ? 16 : 8;  // a row's lanes when partial results are joined
     static_assert(W <= 32 && R * WL <= T, "one lane a warp, one pass over the rows");
     __shared__ float weight[R][WL];
     __shared__ float2 row_ml[R];
-    __shared__ int piece_id[2 * W];  // first unit of the item that a warp's partial result belongs to, or -1
+    constexpr int NONE = -0x7fffffff - 1;
+    __shared__ int piece_id[2 * W];  // first unit of the item that a warp's partial result belongs to, or NONE
     __shared__ int4 piece_item[2 * W][2];  // units, sequence's first token, rows, first row; KV head
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    int* pre = reinterpret_cast<int*>(smem);  // first unit of each sequence, before the rings start
+    long long* pre = reinterpret_cast<long long*>(smem);  // first unit of each sequence, before the rings start
     uint8_t* ring = smem + warp * C::RING;
     float* head_part = a.warp_part + ((long long)blockIdx.x * W + warp) * C::PART;
     float* tail_part = reinterpret_cast<float*>(ring);
@@ -159,63 +160,63 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     pdl_wait();
     pdl_trigger();
     if (lane == 0) {
-        piece_id[2 * warp] = piece_id[2 * warp + 1] = -1;
+        piece_id[2 * warp] = piece_id[2 * warp + 1] = NONE;
     }
 
     // ---- the line of units: its length, this warp's share, where the share begins ----
     // Even shares for the CTAs, then for their warps: a short line still spreads over all SMs.
-    int total = 0, cta_lo, cta_hi, per_cta, u0 = 0, u1 = 0;
+    // All but the line's length and places are counted from the CTA's first unit, cta_lo.
+    long long total = 0, cta_lo = 0;
+    int per_cta = 1, cta_n = 0, u0 = 0, u1 = 0;
     auto shares = [&]() {
-        per_cta = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+        per_cta = quotient(total + gridDim.x - 1, gridDim.x);
         const int per = (per_cta + W - 1) / W;
-        cta_lo = min((long long)total, (long long)blockIdx.x * per_cta);
-        cta_hi = min(total, cta_lo + per_cta);
-        u0 = min(cta_hi, cta_lo + warp * per);
-        u1 = min(cta_hi, u0 + per);
+        cta_lo = min(total, (long long)blockIdx.x * per_cta);
+        cta_n = (int)min(total - cta_lo, (long long)per_cta);
+        u0 = min(cta_n, warp * per);
+        u1 = min(cta_n, u0 + per);
     };
-    // Sums stop at INT_MAX: the entry point bounds them, but only for a q_start that does not decrease;
-    // with any other, every share still begins inside some sequence's items.
-    auto plus = [](int x, int y) -> int { return x > 0x7fffffff - y ? 0x7fffffff : x + y; };
-    auto scan = [&](int u) -> int {  // inclusive over the warp
+    // Sums stop at the most units of a call: the entry point bounds them, but only for a q_start that does
+    // not decrease; with any other, every share still begins inside some sequence's items.
+    const long long most = kv4_most_units(gridDim.x);
+    auto plus = [&](long long x, long long y) -> long long { return min(x + y, most); };
+    auto units_of = [&](const Seq& x) -> long long { return (long long)x.nch * a.Hk * x.nt; };
+    auto scan = [&](long long u) -> long long {  // inclusive over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, u, o);
+            const long long v = __shfl_up_sync(0xffffffffu, u, o);
             if (lane >= o) u = plus(u, v);
         }
         return u;
     };
     Item<R> cur;
     cur.b = 0;
-    int at = 0;  // first unit of sequence cur.b
+    long long seq_at = 0;  // first unit of sequence cur.b, on the line
     if (a.B <= 32) {
         // one sequence a lane: each warp finds its place by itself
         Seq x = {0, 0, 0, 1, 0};
         if (lane < a.B) x = seq_of<R>(a, lane);
-        const int u = x.nt * x.nch * a.Hk, incl = scan(u);
+        const long long u = units_of(x), incl = scan(u);
         total = __shfl_sync(0xffffffffu, incl, 31);
         shares();
         if (u0 < u1) {
-            cur.b = 31 - __clz(__ballot_sync(0xffffffffu, u > 0 && incl - u <= u0));
-            at = __shfl_sync(0xffffffffu, incl - u, cur.b);
+            cur.b = 31 - __clz(__ballot_sync(0xffffffffu, u > 0 && incl - u <= cta_lo + u0));
+            seq_at = __shfl_sync(0xffffffffu, incl - u, cur.b);
             cur.take(x, cur.b);
         }
     } else {
         // T sequences at a time; twice over them when there are more
         for (int turn = 0; turn < 2; ++turn) {
-            int carry = 0;
+            long long carry = 0;
             for (int c = 0; c < a.B; c += T) {
-                int u = 0;
-                if (c + tid < a.B) {
-                    const Seq x = seq_of<R>(a, c + tid);
-                    u = x.nt * x.nch * a.Hk;
-                }
-                int incl = scan(u);
+                const long long u = c + tid < a.B ? units_of(seq_of<R>(a, c + tid)) : 0;
+                long long incl = scan(u);
                 __syncthreads();
                 if (lane == 31) wsum[warp] = incl;
                 __syncthreads();
-                int all = 0;
+                long long all = 0;
                 for (int w = 0; w < W; ++w) {
-                    const int v = wsum[w];
+                    const long long v = wsum[w];
                     if (w < warp) incl = plus(incl, v);
                     all = plus(all, v);
                 }
@@ -225,15 +226,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
                     total = all;
                     shares();
                 }
-                if ((turn == 1 || a.B <= T) && u0 < u1 && pre[0] <= u0) {
-                    int lo = 0, hi = min(T, a.B - c) - 1;  // the last sequence that begins at or before u0
+                const long long mine = cta_lo + u0;
+                if ((turn == 1 || a.B <= T) && u0 < u1 && pre[0] <= mine) {
+                    int lo = 0, hi = min(T, a.B - c) - 1;  // the last sequence that begins at or before this share
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) >> 1;
-                        if (pre[mid] <= u0) lo = mid;
+                        if (pre[mid] <= mine) lo = mid;
                         else hi = mid - 1;
                     }
                     cur.b = c + lo;
-                    at = pre[lo];
+                    seq_at = pre[lo];
                 }
                 carry = plus(carry, all);
             }
@@ -252,11 +254,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     const uint32_t page_bytes = a.Hk * rec.bytes;
 
     if (units > 0) {
-        const int skip = (u0 - at) / cur.s.nt;  // items of the sequence before this share's first
-        int tile = u0 - at - skip * cur.s.nt;
-        cur.kvh = skip / cur.s.nch;
-        cur.chunk = skip - cur.kvh * cur.s.nch;
-        at += skip * cur.s.nt;  // first unit of the current item
+        const long long into = cta_lo + u0 - seq_at;  // units of the sequence before this share's first
+        int tile;
+        if (into <= 0x7fffffff) {
+            const int skip = (int)into / cur.s.nt;  // items
+            tile = (int)into - skip * cur.s.nt;
+            cur.kvh = skip / cur.s.nch;
+            cur.chunk = skip - cur.kvh * cur.s.nch;
+        } else {
+            const long long skip = into / cur.s.nt;
+            tile = (int)(into - skip * cur.s.nt);
+            cur.kvh = (int)(skip / cur.s.nch);
+            cur.chunk = (int)(skip - (long long)cur.kvh * cur.s.nch);
+        }
+        int at = u0 - tile;  // first unit of the current item, below 0 where a CTA before this one began it
 
         // ---- the ring: copies run ST units ahead, the table entries of the one after them too ----
         Item<R> ld = cur;
@@ -591,11 +602,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     // consecutive warps and at the end perhaps the first of the next. Lane w looks at warp w's.
     int4 split = make_int4(0, 0, 0, 0);
     int split_kvh = 0;
-    const int my_head = lane < W ? piece_id[2 * lane] : -1, my_tail = lane < W ? piece_id[2 * lane + 1] : -1;
+    const int my_head = lane < W ? piece_id[2 * lane] : NONE, my_tail = lane < W ? piece_id[2 * lane + 1] : NONE;
     const int before = __shfl_up_sync(0xffffffffu, my_tail, 1);
-    unsigned leaders = __ballot_sync(0xffffffffu, my_tail >= 0 && (lane == 0 || before != my_tail));
+    unsigned leaders = __ballot_sync(0xffffffffu, my_tail != NONE && (lane == 0 || before != my_tail));
     // an item that ends in the first warp's share has no last result here
-    bool alone = __shfl_sync(0xffffffffu, my_head, 0) >= 0;
+    bool alone = __shfl_sync(0xffffffffu, my_head, 0) != NONE;
     while (alone || leaders) {
         const int w_lo = alone ? 0 : __ffs(leaders) - 1, p = 2 * w_lo + (alone ? 0 : 1);
         const int id = __shfl_sync(0xffffffffu, alone ? my_head : my_tail, w_lo);
@@ -606,10 +617,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
         alone = false;
         const int4 it = piece_item[p][0];  // units, first token, rows, first row
         const int kvh = piece_item[p][1].x;
-        const bool whole = id >= cta_lo && id + it.x <= cta_hi;
-        const int tail = id >= cta_lo ? 1 : 0;
+        const bool whole = id >= 0 && id + it.x <= cta_n;
+        const int tail = id >= 0 ? 1 : 0;
         if (!whole && tail) {
-            split = make_int4((id + it.x - 1) / per_cta - (int)blockIdx.x + 1, it.y, it.z, it.w);
+            split = make_int4((id + it.x - 1) / per_cta + 1, it.y, it.z, it.w);
             split_kvh = kvh;
         }
         // every entry but the last is a last result (in shared memory)
@@ -820,10 +831,11 @@ extern "C" int llm_op_attention_kv4(const void* q, const void* pool, int n_pages
 }
 
 int lfw::kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size) {
-    // units are counted in 32 bits, and a row is divided by G as 32-bit fixed point
-    const long long G = H / Hk, chunks = (long long)N * G / 8 + B, tiles = ((long long)max_blocks * page_size + 31) / 32;
-    if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > (1LL << 31) / tiles)
-        return set_error(LLM_ERR_UNSUPPORTED, "more query rows or keys than one call takes");
+    // a row is divided by G as 32-bit fixed point; units: see kv4_most_units; tiles of row blocks are an int
+    const long long G = H / Hk, chunks = (long long)N * G / 8 + B, keys = (long long)max_blocks * page_size;
+    if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > kv4_most_units(current_num_sms()) / ((keys + 31) / 32) ||
+        kv4_prefill_blocks(B, N, (int)G, kFewRows) >= (1LL << 31) / (keys / 128 + 4))
+        return set_error(LLM_ERR_UNSUPPORTED, "more query rows over tables this wide than one call takes");
     return LLM_OK;
 }
 

@@ -54,6 +54,12 @@ struct Kv4AttnArgs {
 // that is for r < 2^32 / G, and rows of a call are fewer (the entry point checks).
 DEVI int div_g(const Kv4AttnArgs& a, int r) { return a.G == 1 ? r : (int)__umulhi((uint32_t)r, a.g_mul); }
 
+// Units of work lie on one line, more of them than 32 bits count where many rows meet many keys. A CTA's share
+// fits an int, and within it units are counted from its first one. Units of a call, at most:
+__host__ __device__ constexpr long long kv4_most_units(int ctas) { return (long long)ctas << 29; }
+// a / b, as 32-bit numbers where they are such.
+DEVI int quotient(long long a, int b) { return a <= 0x7fffffff ? (int)a / b : (int)(a / b); }
+
 // The prompts' kernel. Blocks of a call, at most:
 inline long long kv4_prefill_blocks(int B, int N, int G, int few) {
     const long long rows = (long long)N * G, seqs = rows / (few + 1);

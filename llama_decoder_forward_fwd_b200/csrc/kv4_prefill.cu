@@ -307,17 +307,20 @@ __global__ void __launch_bounds__(KP_LIST) kv4_blocks_kernel(const Kv4AttnArgs a
     }
     // The CTAs' shares: the item in which one begins says where. A share that would begin in an
     // item's fixed cost begins with its first tile.
-    const int units = tiles * a.Hk, per = max(KP_SHARE, (units + sms - 1) / sms), ctas = (units + per - 1) / per;
+    const long long units = (long long)tiles * a.Hk;
+    const int per = max(KP_SHARE, quotient(units + sms - 1, sms)), ctas = quotient(units + per - 1, per);
     if (tid == 0) {
         a.counts[0] = ctas;
         a.counts[1] = listed;
         a.starts[ctas] = make_int4(blocks, 0, 0, 0);
     }
     for (int i = tid; i < blocks; i += KP_LIST) {
-        const int len = a.blocks[i].nkt + item, lo = a.blocks[i].start * a.Hk, hi = lo + len * a.Hk;
-        for (int c = (lo + per - 1) / per; c < ctas && c * per < hi; ++c) {
-            const int off = c * per - lo, kvh = off / len;
-            a.starts[c] = make_int4(i, kvh, max(0, off - kvh * len - item), 0);
+        const int len = a.blocks[i].nkt + item;
+        const long long lo = (long long)a.blocks[i].start * a.Hk, hi = lo + (long long)len * a.Hk;
+        for (int c = quotient(lo + per - 1, per); c < ctas && (long long)c * per < hi; ++c) {
+            const long long off = (long long)c * per - lo;
+            const int kvh = quotient(off, len);
+            a.starts[c] = make_int4(i, kvh, max(0, (int)(off - (long long)kvh * len) - item), 0);
         }
     }
 }

@@ -1,0 +1,48 @@
+"""Attention over the 4-bit cache in large calls (GPU): schedules of more than 2^31 units."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _held(pool, Hk, d, P, which, g):
+    """Values of KV head g of a pool whose pages lie in order, float64 [tokens, d]."""
+    rec = pool.view(pool.shape[0], Hk, -1)[:, g]
+    a, b = P * d // 2, P * d // 8
+    c = rec[:, which * a:(which + 1) * a].reshape(-1, d // 2)
+    sz = rec[:, 2 * a + which * b:2 * a + (which + 1) * b].reshape(-1, d // 8).view(torch.bfloat16).double()
+    c = torch.stack((c & 15, c >> 4), -1).reshape(-1, d // 32, 32).double()
+    return (c * sz[:, 0::2, None] + sz[:, 1::2, None]).to(torch.bfloat16).double().reshape(-1, d)
+
+
+def test_more_units_than_32_bits_count(lib):
+    """131k new tokens over their own keys, announced as one: 8 of their 4 x 131k rows at a time pass over all keys."""
+    import llama_decoder_forward_fwd_b200 as L
+    N, H, Hk, d, P = 132096, 32, 8, 64, 128
+    assert (N * H // Hk // 8) * Hk * (N // 32) > 2**31
+    g = torch.Generator(device=DEV).manual_seed(3)
+    n_pages = N // P
+    pool = torch.randint(0, 256, (n_pages, L.llm_kv4_page_bytes(Hk, d, P)), dtype=torch.uint8, device=DEV, generator=g)
+    rec = pool.view(n_pages, Hk, -1)
+    pairs = P * d // 8 * 2
+    sz = (torch.rand(n_pages, Hk, pairs // 4, 2, device=DEV, generator=g) * torch.tensor([0.2, -2.0], device=DEV)).to(torch.bfloat16)
+    rec[:, :, -pairs:] = sz.view(torch.uint8).reshape(n_pages, Hk, pairs)
+    q = torch.randn(N, H, d, device=DEV, generator=g).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table, lens = torch.arange(n_pages, **i32)[None].contiguous(), torch.tensor([N], **i32)
+    q_start, out = torch.tensor([0, N], **i32), torch.zeros(N, H * d, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(L.llm_op_attention_kv4_workspace(1, N, 1, H, Hk, d, n_pages, P), dtype=torch.uint8, device=DEV)
+    L.llm_op_attention_kv4(q, pool, P, Hk, table, lens, q_start, 1, out, ws)
+    L.llm_op_synchronize()
+    rows = torch.tensor([0, 1, 31, 32, 4095, 40000, 65535, 65536, 100001, 128000, N - 2, N - 1], device=DEV)
+    mask = torch.arange(N, device=DEV)[None] > rows[:, None]
+    for h in (0, 7, 17, H - 1):
+        k, v = (_held(pool, Hk, d, P, w, h // 4) for w in (0, 1))
+        w = torch.softmax((q[rows, h].double() @ k.T / math.sqrt(d)).masked_fill(mask, -math.inf), -1)
+        want = w @ v
+        bound = 2.0**-8 * want.abs() + (2.0**-8 + 2.0**-11) * (w @ v.abs())
+        got = out[rows, h * d:(h + 1) * d].double()
+        assert ((got - want).abs() <= bound).all(), h

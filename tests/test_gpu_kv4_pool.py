@@ -30,7 +30,7 @@ def test_refused_calls_take_no_pages(lib):
     there were, what follows is as in a model that never had one."""
     import llama_decoder_forward_fwd_b200 as L
     shape = BASE.replace(dim=1024, n_heads=16, n_kv_heads=2, head_dim=64, max_seq_len=1 << 25)
-    T = 33000
+    T = 40000
     m = _model(shape, 1, T)
     x, nxt = torch.zeros(1, T, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
     for _ in range((1 << 25) // T + 2):

@@ -475,9 +475,11 @@ int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void* v, int64_t
  * (NaN and infinities included).
  * workspace: device scratch of llm_op_attention_kv4_workspace(...) bytes (0 for a bad
  * shape), 16-byte aligned, contents arbitrary; calls sharing one must not overlap in time.
- * From some 1000 query rows per KV head and sequence on, up to 1 GiB of it is room to expand the prompts' cache
- * to bf16 once; a call that is given less, but what it needs without, expands the codes for each 128 rows again
- * (and sums in another order).
+ * From some 1000 query rows per KV head and sequence on, part of it is room to expand the
+ * prompts' cache to bf16 once: what tables filled to their width would need, or 64 MiB where
+ * that passes 1 GiB. A call uses what room it is given beyond its least (that of max_new =
+ * 1000 Hk/H), up to 1 GiB; prompts that find none are expanded for each 128 rows again (and sum
+ * in another order).
  * Errors: as above, and LLM_ERR_UNSUPPORTED for more than one call takes, which goes by the
  * tables' width and not by the lengths: N (H/Hk)^2 from 2^31 on, or (N H / 8 + B Hk)
  * ceil(max_blocks page_size / 32) above 2^29 per SM (2^36 on a B200: 2M new tokens of 32 heads

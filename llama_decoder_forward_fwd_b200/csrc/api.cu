@@ -832,7 +832,7 @@ int llm_model_init(const llm_config* cfg, const llm_weights* w, void* stream, ll
         m->kv_layer_bytes = (size_t)m->kv_pages * llm_kv4_page_bytes(Hk, d, kKv4Page);
         // the largest workspace of any call: it depends on the rows per KV head up to the prompts' threshold
         for (int T = 1; T <= m->M_max; T = T < 128 ? T + 1 : T < m->M_max ? m->M_max : T + 1) {
-            const size_t b = llm_op_attention_kv4_workspace(c.max_batch, m->M_max, T, H, Hk, d, m->kv_blocks, kKv4Page);
+            const size_t b = attention_kv4_most_workspace(c.max_batch, m->M_max, T, H, Hk, d, m->kv_blocks, kKv4Page);
             m->kv_ws_bytes = b > m->kv_ws_bytes ? b : m->kv_ws_bytes;
         }
         MALLOC_OR_BAIL(m->kv_pool, c.n_layers * m->kv_layer_bytes);

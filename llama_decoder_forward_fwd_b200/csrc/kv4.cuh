@@ -81,6 +81,8 @@ struct Kv4StoreArgs {
 cudaError_t launch_kv4_store(const Kv4StoreArgs& a, int d, cudaStream_t s);
 // LLM_OK, or why a call of these sizes is more than llm_op_attention_kv4 takes.
 int kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size);
+// Workspace with room for all the expanded tiles that a call of these sizes, or a smaller one, may use.
+size_t attention_kv4_most_workspace(int B, int N, int max_new, int H, int Hk, int d, int max_blocks, int page_size);
 // llm_op_attention_kv4 with the error word of the caller's model.
 int attention_kv4(const void* q, const void* pool, int n_pages, int page_size, const int32_t* table, int max_blocks,
                   const int32_t* lens, const int32_t* q_start, int B, int N, int max_new, int H, int Hk, int d, void* out,

@@ -747,6 +747,16 @@ bool has_prompts(int max_new, int G) { return (long long)max_new * G > kFewRows;
 // with one KV head, 1024 rows 31 / 41.
 constexpr int kImageRows = 1024;
 bool has_images(int max_new, int G) { return (long long)max_new * G > kImageRows; }
+// Room for the expanded tiles: at most 1 GiB. The lengths are on the device, so a workspace is asked for
+// by the tables' width; where that passes the most, the lengths are likely to be far below it: 64 MiB are asked for
+// then (16k keys of 8 KV heads of 128), and what a caller gives beyond is used. Prompts that find no room are
+// expanded row block by row block, in a second turn of the kernels: 7 us more where all had room (192 us for 4 prompts of
+// 2048 tokens, 8 KV heads, tables of 131k tokens; 185 us with tables that fit).
+constexpr long long kMostImageBytes = 1LL << 30, kSomeImageBytes = 1LL << 26;
+int images_within(long long images, int d, long long bytes) {
+    const long long room = bytes / (512 * d);
+    return (int)(images < room ? images : room);
+}
 // Row tiles of 8 per item: as many as the longest sequence's rows need, at most 4 (the
 // accumulators fill the registers). Beside prompts the others mostly decode.
 int row_tiles(int max_new, int G) {
@@ -754,15 +764,15 @@ int row_tiles(int max_new, int G) {
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-// Workspace: CTAs' parts | their maxima and sums | warps' parts | split items; with prompts their row blocks, shares and
-// parts | marks of odd sequences; with `images` what they are expanded to.
+// Workspace: CTAs' parts | their maxima and sums | warps' parts | split items; with prompts their row blocks and shares |
+// marks of odd sequences | what they are expanded to, n_images tiles | their parts.
 struct Ws {
     size_t ml, warp, desc, blocks, starts, splits, p_part, p_ml, odd, expanded, holes, images, bytes;
     long long cap;  // row blocks of the prompts' kernel
-    int n_images;   // its expanded tiles
 };
-Ws ws_layout(int grid, int nt, int d, int B, int N, int G, int Hk, long long max_keys, bool prompts, bool images) {
+Ws ws_layout(int grid, int nt, int d, int B, int N, int G, bool prompts, int n_images) {
     const size_t slots = (size_t)grid * 2, R = 8 * nt, warps = (size_t)grid * ka_warps(nt);
+    auto up16 = [](size_t x) { return (x + 15) & ~size_t(15); };
     Ws w = {};
     w.ml = slots * R * d * 4;
     w.warp = w.ml + slots * R * 8;
@@ -776,20 +786,27 @@ Ws ws_layout(int grid, int nt, int d, int B, int N, int G, int Hk, long long max
     w.cap = kv4_prefill_blocks(B, N, G, kFewRows);
     w.starts = w.blocks + (size_t)w.cap * sizeof(Kv4Block);
     w.splits = w.starts + (size_t)(grid + 1) * 16;
-    w.p_part = w.splits + (size_t)grid * sizeof(Kv4Split);
-    w.p_ml = w.p_part + slots * 128 * d * 4;
-    w.odd = w.p_ml + slots * 128 * 8;
-    w.bytes = w.odd + (size_t)(B + 2) * 4;
-    if (!images) return w;
-    w.n_images = kv4_images(B, N, G, Hk, d, max_keys, kFewRows);
-    if (w.n_images == 0) return w;
-    w.expanded = (w.bytes + 15) & ~size_t(15);
-    w.holes = w.expanded + (size_t)kv4_expanded_seqs(B, N, G, kFewRows) * sizeof(Kv4Expanded);
-    w.images = (w.holes + (size_t)w.n_images * 8 + 15) & ~size_t(15);
-    w.p_part = w.images + (size_t)w.n_images * 512 * d;  // of 256 rows each then
-    w.p_ml = w.p_part + slots * 256 * d * 4;
-    w.bytes = w.p_ml + slots * 256 * 8;
+    w.odd = w.splits + (size_t)grid * sizeof(Kv4Split);
+    w.p_part = up16(w.odd + (size_t)(B + 2) * 4);
+    if (n_images) {
+        w.expanded = w.p_part;
+        w.holes = w.expanded + (size_t)kv4_expanded_seqs(B, N, G, kFewRows) * sizeof(Kv4Expanded);
+        w.images = up16(w.holes + (size_t)n_images * 8);
+        w.p_part = w.images + (size_t)n_images * 512 * d;
+    }
+    const size_t rows = n_images ? 256 : 128;  // of a block
+    w.p_ml = w.p_part + slots * rows * d * 4;
+    w.bytes = w.p_ml + slots * rows * 8;
     return w;
+}
+// The tiles that fit into a workspace of so many bytes, `images` at most; fewer than a sequence needs are none.
+int images_in(size_t bytes, int images, int grid, int nt, int d, int B, int N, int G, int Hk) {
+    auto need = [&](int n) { return ws_layout(grid, nt, d, B, N, G, true, n).bytes; };
+    if (images < Hk || bytes < need(Hk)) return 0;
+    const size_t more = (bytes - need(Hk)) / (512 * d + 8) + 2;  // one too many at least, but for the padding
+    int n = more < (size_t)(images - Hk) ? Hk + (int)more : images;
+    while (need(n) > bytes) --n;
+    return n;
 }
 
 template <int D, int NT> cudaError_t launch_attn(const Kv4AttnArgs& a, int grid, cudaStream_t s) {
@@ -814,12 +831,22 @@ int check_shape(int B, int N, int max_new, int H, int Hk, int d, int max_blocks,
 
 using namespace lfw;
 
+static size_t kv4_workspace(int B, int N, int max_new, int H, int Hk, int d, int max_blocks, int page_size, bool most) {
+    if (check_shape(B, N, max_new, H, Hk, d, max_blocks, page_size) != LLM_OK) return 0;
+    const int G = H / Hk;
+    const long long all = has_images(max_new, G) ? kv4_images(B, N, G, Hk, (long long)max_blocks * page_size, kFewRows) : 0;
+    const int fit = images_within(all, d, kMostImageBytes);
+    return ws_layout(current_num_sms(), row_tiles(max_new, G), d, B, N, G, has_prompts(max_new, G),
+                     most || fit == all ? fit : images_within(all, d, kSomeImageBytes)).bytes;
+}
+
 extern "C" size_t llm_op_attention_kv4_workspace(int B, int N, int max_new, int H, int Hk, int d, int max_blocks,
                                                  int page_size) {
-    if (check_shape(B, N, max_new, H, Hk, d, max_blocks, page_size) != LLM_OK) return 0;
-    const int nt = row_tiles(max_new, H / Hk);
-    return ws_layout(current_num_sms(), nt, d, B, N, H / Hk, Hk, (long long)max_blocks * page_size, has_prompts(max_new, H / Hk),
-                     has_images(max_new, H / Hk)).bytes;
+    return kv4_workspace(B, N, max_new, H, Hk, d, max_blocks, page_size, false);
+}
+
+size_t lfw::attention_kv4_most_workspace(int B, int N, int max_new, int H, int Hk, int d, int max_blocks, int page_size) {
+    return kv4_workspace(B, N, max_new, H, Hk, d, max_blocks, page_size, true);
 }
 
 extern "C" int llm_op_attention_kv4(const void* q, const void* pool, int n_pages, int page_size, const int32_t* table,
@@ -854,9 +881,11 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
         return set_error(LLM_ERR_BAD_ARG, "operands must be 16-byte aligned");
     const int nt = row_tiles(max_new, H / Hk), grid = current_num_sms();
     const bool prompts = has_prompts(max_new, H / Hk);
-    auto layout = [&](bool images) { return ws_layout(grid, nt, d, B, N, H / Hk, Hk, (long long)max_blocks * page_size, prompts, images); };
-    Ws w = layout(has_images(max_new, H / Hk));
-    if (workspace_bytes < w.bytes) w = layout(false);
+    const long long all_images =
+        has_images(max_new, H / Hk) ? kv4_images(B, N, H / Hk, Hk, (long long)max_blocks * page_size, kFewRows) : 0;
+    const int n_images =
+        images_in(workspace_bytes, images_within(all_images, d, kMostImageBytes), grid, nt, d, B, N, H / Hk, Hk);
+    const Ws w = ws_layout(grid, nt, d, B, N, H / Hk, prompts, n_images);
     if (workspace_bytes < w.bytes) return set_error(LLM_ERR_BAD_ARG, "workspace too small");
     Kv4AttnArgs a;
     a.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -890,8 +919,9 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
     a.expanded = reinterpret_cast<Kv4Expanded*>(base + w.expanded);
     a.holes = reinterpret_cast<uint64_t*>(base + w.holes);
     a.images = reinterpret_cast<uint8_t*>(base + w.images);
-    a.images_cap = w.n_images;
-    a.expanded_cap = w.n_images ? kv4_expanded_seqs(B, N, H / Hk, kFewRows) : 0;
+    a.images_cap = n_images;
+    a.expanded_cap = n_images ? kv4_expanded_seqs(B, N, H / Hk, kFewRows) : 0;
+    a.turn = n_images && n_images < all_images ? 1 : 0;
     a.p_part = reinterpret_cast<float*>(base + w.p_part);
     a.p_ml = reinterpret_cast<float*>(base + w.p_ml);
     a.err = err || !prompts ? err : op_err_word();  // only the prompts' kernel waits on barriers

@@ -36,12 +36,16 @@ struct Kv4AttnArgs {
     int4* desc;    // [CTA][2]: the split item that begins in it: parts, sequence's first token, rows, first row; KV head
     // sequences of more than `few` rows per KV head are the prompts' kernel's, unless it marks them
     int few;
-    int* odd;          // [B]: nonzero for a sequence with a pair that is not finite, null without that kernel
+    int* odd;          // [B]: nonzero for a sequence that is the streaming kernel's all the same, since it has a pair
+                       // that is not finite (KV4_REST between the turns: it had no room); null without that kernel
     Kv4Block* blocks;  // the prompts' row blocks
     int* counts;       // of CTAs with a share, of expanded sequences
     int4* starts;      // [CTAs + 1]: block, KV head and tile that a share begins with
     Kv4Split* splits;  // [CTA]
     int blocks_cap, expanded_cap, images_cap;
+    // Where the prompts may ask for more tiles than there is room for, their kernels run twice: 1, for those that
+    // have room, then 2, for the others, row block by row block. 0: all have room, or none.
+    int turn;
     Kv4Expanded* expanded;
     uint8_t* images;    // [tile][K, V], each as the tensor cores read it
     uint64_t* holes;    // [tile]: which 16-key parts have no page, a byte each
@@ -49,6 +53,8 @@ struct Kv4AttnArgs {
     float* p_ml;       // [CTA][began before, goes on after][rows of a block][2]
     uint32_t* err;
 };
+
+constexpr int KV4_REST = 2;
 
 // r / G for 0 <= r < 2^31: g_mul is ceil(2^32 / G), exact while r * (g_mul G - 2^32) < 2^32,
 // that is for r < 2^32 / G, and rows of a call are fewer (the entry point checks).
@@ -65,15 +71,14 @@ inline long long kv4_prefill_blocks(int B, int N, int G, int few) {
     const long long rows = (long long)N * G, seqs = rows / (few + 1);
     return rows / 128 + (seqs < B ? seqs : B) + 1;
 }
-// Where some sequence has many row blocks, all of the prompts are expanded before, once. Sequences and
-// tiles of that, at most; 0 tiles where the page tables would let them pass 1 GiB.
+// Where some sequence has many row blocks, the prompts are expanded before, once. Sequences and tiles of
+// that, at most (the tiles by the tables' width, the lengths being on the device).
 inline int kv4_expanded_seqs(int B, int N, int G, int few) {
     const long long n = (long long)N * G / (few + 1);
     return (int)(n < B ? n : B);
 }
-inline int kv4_images(int B, int N, int G, int Hk, int d, long long max_keys, int few) {
-    const long long n = kv4_expanded_seqs(B, N, G, few) * ((max_keys + 127) / 128) * Hk;
-    return n * 512 * d <= 1LL << 30 ? (int)n : 0;
+inline long long kv4_images(int B, int N, int G, int Hk, long long max_keys, int few) {
+    return (long long)kv4_expanded_seqs(B, N, G, few) * ((max_keys + 127) / 128) * Hk;
 }
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs& a, int d, cudaStream_t s);
 

@@ -219,8 +219,8 @@ template <int D> DEVI void stage_q(const Kv4AttnArgs& a, const Work& it, int fro
     }
 }
 
-// The row blocks of all sequences with more than a.few rows, the CTAs' shares of their tiles, and
-// the marks of odd sequences cleared. One CTA.
+// The row blocks of all sequences with more than a.few rows that this turn takes, the CTAs' shares of their
+// tiles, and the marks of odd sequences cleared. One CTA.
 __global__ void __launch_bounds__(KP_LIST) kv4_blocks_kernel(const Kv4AttnArgs a, int sms, int block_rows) {
     __shared__ int wsum[KP_LIST / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,21 +256,23 @@ __global__ void __launch_bounds__(KP_LIST) kv4_blocks_kernel(const Kv4AttnArgs a
             len = min(max(a.lens[b], 0), a.max_blocks << a.lp);
             q0 = min(max(x0, 0), a.N);
             n = min(max(x1, q0), a.N) - q0;
-            a.odd[b] = 0;
         }
         const int rows = n * a.G;
         int nb = rows > a.few ? (rows + block_rows - 1) / block_rows : 0, all, all_images, all_listed, image = -1;
+        if (b < a.B && a.turn == 2 && a.odd[b] != KV4_REST) nb = 0;
+        else if (b < a.B) a.odd[b] = 0;
         if (a.images_cap > 0) {
-            // There is room for its images unless q_start decreases somewhere; then the streaming kernel takes it.
-            const int tiles = nb ? max(1, (len + KP_KT - 1) / KP_KT) : 0;
-            image = images + scan(tiles * a.Hk, all_images) - tiles * a.Hk;
-            bool fits = nb > 0 && image >= 0 && image + tiles * a.Hk <= a.images_cap;
+            // A sequence's tiles, or one more than there is room for: those before the first without room are listed.
+            const int tiles = max(1, (len + KP_KT - 1) / KP_KT);
+            const int ask = nb ? (int)min((long long)tiles * a.Hk, a.images_cap + 1LL) : 0;
+            image = images + scan(ask, all_images) - ask;
+            bool fits = nb > 0 && image + ask <= a.images_cap;
             const int li = listed + scan(fits, all_listed) - (fits ? 1 : 0);
-            fits = fits && li < a.expanded_cap;
+            fits = fits && li < a.expanded_cap;  // always, unless q_start decreases somewhere
             if (fits) {
                 a.expanded[li] = Kv4Expanded{b, len, image, tiles};
             } else if (nb > 0) {
-                a.odd[b] = 1;
+                a.odd[b] = a.turn == 1 ? KV4_REST : 1;
                 nb = 0;
             }
             images = min(images + all_images, a.images_cap);
@@ -350,7 +352,6 @@ template <int D> __global__ void __launch_bounds__(256) kv4_expand_kernel(const 
         }
         const Kv4Expanded e = a.expanded[lo];
         const int kvh = (img - e.image) / e.tiles, tile = img - e.image - kvh * e.tiles;
-        if (kvh >= a.Hk) continue;  // between two sequences, where one did not fit
         if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile has been read
         __syncthreads();
         bool odd = false;
@@ -1165,7 +1166,12 @@ template <int D> cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = launch_k(kv4_expanded_kernel<D>, dim3(sms), dim3(KQ_THREADS), kq_smem<D>(), s, true, a);
     if (e != cudaSuccess) return e;
-    return launch_k(kv4_prefill_join_kernel<D, KQ_ROWS>, dim3(sms, D / 16), dim3(KQ_ROWS), 0, s, true, a);
+    e = launch_k(kv4_prefill_join_kernel<D, KQ_ROWS>, dim3(sms, D / 16), dim3(KQ_ROWS), 0, s, true, a);
+    if (e != cudaSuccess || a.turn == 0) return e;
+    Kv4AttnArgs rest = a;
+    rest.images_cap = 0;
+    rest.turn = 2;
+    return launch<D>(rest, s);
 }
 
 }  // namespace

@@ -1,8 +1,12 @@
-"""Attention over the 4-bit cache in large calls (GPU): schedules of more than 2^31 units."""
+"""Attention over the 4-bit cache in large calls (GPU): schedules of more than 2^31 units, page tables much wider than the
+sequences, workspaces with room for some of the prompts."""
 import math
 
+import numpy as np
 import pytest
 import torch
+
+from kv4_case import MANY, Case, marked
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -46,3 +50,36 @@ def test_more_units_than_32_bits_count(lib):
         bound = 2.0**-8 * want.abs() + (2.0**-8 + 2.0**-11) * (w @ v.abs())
         got = out[rows, h * d:(h + 1) * d].double()
         assert ((got - want).abs() <= bound).all(), h
+
+
+@pytest.mark.parametrize("d,P", [(128, 128), (64, 64)])
+def test_wide_page_tables_do_not_change_the_kernel(lib, d, P):
+    """Prompts whose tables reach 270k tokens are expanded like those of tables that fit them: the same bits."""
+    import llama_decoder_forward_fwd_b200 as L
+    lens, new = [600, 450, 40], [500, 450, 1]
+    outs = []
+    for blocks in (5 * 128 // P, 270000 // P):
+        case = Case(lens, new, 8, 4, d, P, 9, blocks=blocks)
+        outs.append(case.run(L, MANY))
+        case.check(outs[-1])
+    assert np.array_equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("d,P,lens,new", [(128, 16, [300, 140, 700, 40, 90], [150, 140, 300, 1, 20]),
+                                          (64, 64, [700, 130, 260], [500, 130, 3])])
+def test_a_workspace_with_room_for_some_of_the_prompts(lib, d, P, lens, new):
+    """From none of the expanded tiles to all of them: what has no room is expanded row block by row block."""
+    import llama_decoder_forward_fwd_b200 as L
+    case = Case(lens, new, 8, 2, d, P, 10, make=marked(2, d, lens), q_scale=0.1, pad=1)
+    shape = (len(lens), case.N + 1)
+    full = L.llm_op_attention_kv4_workspace(*shape, MANY, 8, 2, d, case.blocks, P)
+    least = L.llm_op_attention_kv4_workspace(*shape, 200, 8, 2, d, case.blocks, P)
+    assert least < full
+    most = min(shape[0], shape[1] * 4 // 65) * -(-case.blocks * P // 128) * 2  # tiles that tables so wide may ask for
+    sizes = {least, least + 1, full - 1, full, full + 100000}
+    sizes |= {full - (most - n) * (512 * d + 8) for n in (1, 2, 4, 6, 7, 10, 12, 15, 18, 22, 24, 30)}
+    for room in sorted(x for x in sizes if x >= least):
+        case.check(case.run(L, MANY, room=room))
+    with pytest.raises(L.LlmError) as e:
+        case.run(L, MANY, room=least - 1)
+    assert e.value.code == L.LLM_ERR_BAD_ARG

@@ -1,4 +1,5 @@
-"""The model's own 4-bit cache (LLM_FLAG_KV4): its pages after refused calls and from step to step (GPU)."""
+"""The model's own 4-bit cache (LLM_FLAG_KV4): its pages after refused calls and from step to step, and
+prompts of a model with room for many long sequences (GPU)."""
 import pytest
 import torch
 
@@ -67,3 +68,17 @@ def test_pages_follow_the_lengths(lib):
             L.llm_kv_cache_reset(x.h)
     for x in (m, *one):
         x.free()
+
+
+def test_room_for_many_long_sequences_keeps_the_prompt_kernel(lib):
+    """A prompt gives the same bits in a model of 16 sequences of 36k positions as in one made for it alone."""
+    import llama_decoder_forward_fwd_b200 as L
+    shape = BASE.replace(dim=2048, n_heads=32, n_kv_heads=8, head_dim=64, vocab=256)
+    T = 600
+    tokens = S.make_tokens(13, 1, T, shape.vocab)
+    got = []
+    for seq, batch in ((640, 1), (36864, 16)):
+        m = _model(shape.replace(max_seq_len=seq), batch, T)
+        got.append(_prefill(L, m, tokens))
+        m.free()
+    assert torch.equal(*got)

@@ -40,3 +40,15 @@ def test_large_steps_are_taken(lib, kw):
 def test_steps_that_are_too_large_are_refused(lib, kw):
     rc, why = _attend(lib, **kw)
     assert rc == L.LLM_ERR_UNSUPPORTED and "one call" in why, why
+
+
+def test_the_workspace_of_expanded_prompts_is_bounded(lib):
+    """By the tables' width while that stays within 1 GiB, by 64 MiB beyond; with what else a call needs, some 50 MiB."""
+    def size(B, tokens, Hk=8):
+        return lib.llm_op_attention_kv4_workspace(B, 4096, 2048, 4 * Hk, Hk, 128, -(-tokens // 64), 64)
+    last = 0
+    for tokens in (2048, 8192, 16384, 65536):
+        assert last < size(2, tokens) < (2 * tokens // 128 * 8 << 16) + (50 << 20)
+        last = size(2, tokens)
+    for B, tokens in ((3, 131072), (16, 32768), (2, 1 << 24), (64, 1 << 20)):
+        assert (64 << 20) < size(B, tokens) < (64 + 50 << 20)

@@ -134,7 +134,8 @@ template <int R> struct Item {
     }
 };
 
-template <int D, int NT>
+// I: the type that the line's units are counted in.
+template <int D, int NT, typename I>
 __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(const Kv4AttnArgs a) {
     using C = Cfg<D, NT>;
     constexpr int W = C::WARPS, R = C::R, ST = C::STAGES, T = W * 32;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     constexpr int VW = D / 64;   // and per key of V
     constexpr int MT = D / 16;   // 16-row tiles of O^T
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long wsum[W];
+    __shared__ I wsum[W];
     constexpr int WL = W > 16 ? 32 : W > 8 ? 16 : 8;  // a row's lanes when partial results are joined
     static_assert(W <= 32 && R * WL <= T, "one lane a warp, one pass over the rows");
     __shared__ float weight[R][WL];
@@ -152,7 +153,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
     __shared__ int4 piece_item[2 * W][2];  // units, sequence's first token, rows, first row; KV head
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    long long* pre = reinterpret_cast<long long*>(smem);  // first unit of each sequence, before the rings start
     uint8_t* ring = smem + warp * C::RING;
     float* head_part = a.warp_part + ((long long)blockIdx.x * W + warp) * C::PART;
     float* tail_part = reinterpret_cast<float*>(ring);
@@ -165,38 +165,37 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
 
     // ---- the line of units: its length, this warp's share, where the share begins ----
     // Even shares for the CTAs, then for their warps: a short line still spreads over all SMs.
-    // All but the line's length and places are counted from the CTA's first unit, cta_lo.
-    long long total = 0, cta_lo = 0;
-    int per_cta = 1, cta_n = 0, u0 = 0, u1 = 0;
+    // What follows the schedule counts from the CTA's first unit.
+    int per_cta = 1, cta_n = 0, u0 = 0, u1 = 0, tile = 0;
+    Item<R> cur;
+    cur.b = 0;
+    I total = 0, cta_lo = 0, seq_at = 0;  // units of the line, the CTA's first, the first of sequence cur.b
     auto shares = [&]() {
-        per_cta = quotient(total + gridDim.x - 1, gridDim.x);
+        per_cta = div_up(total, gridDim.x);
         const int per = (per_cta + W - 1) / W;
-        cta_lo = min(total, (long long)blockIdx.x * per_cta);
-        cta_n = (int)min(total - cta_lo, (long long)per_cta);
+        cta_lo = (I)min((long long)total, (long long)blockIdx.x * per_cta);
+        cta_n = (int)min(total - cta_lo, (I)per_cta);
         u0 = min(cta_n, warp * per);
         u1 = min(cta_n, u0 + per);
     };
     // Sums stop at the most units of a call: the entry point bounds them, but only for a q_start that does
     // not decrease; with any other, every share still begins inside some sequence's items.
-    const long long most = kv4_most_units(gridDim.x);
-    auto plus = [&](long long x, long long y) -> long long { return min(x + y, most); };
-    auto units_of = [&](const Seq& x) -> long long { return (long long)x.nch * a.Hk * x.nt; };
-    auto scan = [&](long long u) -> long long {  // inclusive over the warp
+    const I most = sizeof(I) == 4 ? (I)0x7fffffff : (I)kv4_most_units(gridDim.x);
+    auto plus = [&](I x, I y) -> I { return x > most - y ? most : x + y; };
+    auto units_of = [&](const Seq& x) -> I { return (I)x.nch * a.Hk * x.nt; };
+    auto scan = [&](I u) -> I {  // inclusive over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, u, o);
+            const I v = __shfl_up_sync(0xffffffffu, u, o);
             if (lane >= o) u = plus(u, v);
         }
         return u;
     };
-    Item<R> cur;
-    cur.b = 0;
-    long long seq_at = 0;  // first unit of sequence cur.b, on the line
     if (a.B <= 32) {
         // one sequence a lane: each warp finds its place by itself
         Seq x = {0, 0, 0, 1, 0};
         if (lane < a.B) x = seq_of<R>(a, lane);
-        const long long u = units_of(x), incl = scan(u);
+        const I u = units_of(x), incl = scan(u);
         total = __shfl_sync(0xffffffffu, incl, 31);
         shares();
         if (u0 < u1) {
@@ -206,17 +205,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
         }
     } else {
         // T sequences at a time; twice over them when there are more
+        I* pre = reinterpret_cast<I*>(smem);  // first unit of each, before the rings start
         for (int turn = 0; turn < 2; ++turn) {
-            long long carry = 0;
+            I carry = 0;
             for (int c = 0; c < a.B; c += T) {
-                const long long u = c + tid < a.B ? units_of(seq_of<R>(a, c + tid)) : 0;
-                long long incl = scan(u);
+                const I u = c + tid < a.B ? units_of(seq_of<R>(a, c + tid)) : 0;
+                I incl = scan(u);
                 __syncthreads();
                 if (lane == 31) wsum[warp] = incl;
                 __syncthreads();
-                long long all = 0;
+                I all = 0;
                 for (int w = 0; w < W; ++w) {
-                    const long long v = wsum[w];
+                    const I v = wsum[w];
                     if (w < warp) incl = plus(incl, v);
                     all = plus(all, v);
                 }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
                     total = all;
                     shares();
                 }
-                const long long mine = cta_lo + u0;
+                const I mine = cta_lo + u0;
                 if ((turn == 1 || a.B <= T) && u0 < u1 && pre[0] <= mine) {
                     int lo = 0, hi = min(T, a.B - c) - 1;  // the last sequence that begins at or before this share
                     while (lo < hi) {
@@ -249,24 +249,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
         cur.b = __shfl_sync(0xffffffffu, cur.b, 0);
         if (u0 < u1) cur.take(seq_of<R>(a, cur.b), 0);
     }
+    if (u0 < u1) {
+        const I into = cta_lo + u0 - seq_at, skip = into / cur.s.nt;  // units and items of the sequence before this share
+        tile = (int)(into - skip * cur.s.nt);
+        cur.kvh = (int)(skip / cur.s.nch);
+        cur.chunk = (int)(skip - (I)cur.kvh * cur.s.nch);
+    }
     const int units = u1 - u0;
     const Kv4Rec rec = kv4_rec(1 << a.lp, D);
     const uint32_t page_bytes = a.Hk * rec.bytes;
 
     if (units > 0) {
-        const long long into = cta_lo + u0 - seq_at;  // units of the sequence before this share's first
-        int tile;
-        if (into <= 0x7fffffff) {
-            const int skip = (int)into / cur.s.nt;  // items
-            tile = (int)into - skip * cur.s.nt;
-            cur.kvh = skip / cur.s.nch;
-            cur.chunk = skip - cur.kvh * cur.s.nch;
-        } else {
-            const long long skip = into / cur.s.nt;
-            tile = (int)(into - skip * cur.s.nt);
-            cur.kvh = (int)(skip / cur.s.nch);
-            cur.chunk = (int)(skip - (long long)cur.kvh * cur.s.nch);
-        }
         int at = u0 - tile;  // first unit of the current item, below 0 where a CTA before this one began it
 
         // ---- the ring: copies run ST units ahead, the table entries of the one after them too ----
@@ -809,11 +802,12 @@ int images_in(size_t bytes, int images, int grid, int nt, int d, int B, int N, i
     return n;
 }
 
-template <int D, int NT> cudaError_t launch_attn(const Kv4AttnArgs& a, int grid, cudaStream_t s) {
+template <int D, int NT> cudaError_t launch_attn(const Kv4AttnArgs& a, bool wide, int grid, cudaStream_t s) {
     using C = Cfg<D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    auto* kernel = wide ? kv4_attn_kernel<D, NT, long long> : kv4_attn_kernel<D, NT, int>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_k(kv4_attn_kernel<D, NT>, dim3(grid), dim3(C::WARPS * 32), C::SMEM, s, true, a);
+    e = launch_k(kernel, dim3(grid), dim3(C::WARPS * 32), C::SMEM, s, true, a);
     if (e != cudaSuccess) return e;
     return launch_k(kv4_attn_join_kernel<D, NT>, dim3(grid, 4 * NT), dim3(256), 0, s, true, a);
 }
@@ -860,7 +854,7 @@ extern "C" int llm_op_attention_kv4(const void* q, const void* pool, int n_pages
 int lfw::kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size) {
     // a row is divided by G as 32-bit fixed point; units: see kv4_most_units; tiles of row blocks are an int
     const long long G = H / Hk, chunks = (long long)N * G / 8 + B, keys = (long long)max_blocks * page_size;
-    if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > kv4_most_units(current_num_sms()) / ((keys + 31) / 32) ||
+    if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > kv4_most_units(current_num_sms()) / ((keys + KA_KEYS - 1) / KA_KEYS) ||
         kv4_prefill_blocks(B, N, (int)G, kFewRows) >= (1LL << 31) / (keys / 128 + 4))
         return set_error(LLM_ERR_UNSUPPORTED, "more query rows over tables this wide than one call takes");
     return LLM_OK;
@@ -902,6 +896,7 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
     a.H = H;
     a.Hk = Hk;
     a.G = H / Hk;
+    const bool wide = ((long long)N * a.G / 8 + B) * Hk * (((long long)max_blocks * page_size + KA_KEYS - 1) / KA_KEYS) >= 1LL << 31;
     a.g_mul = a.G > 1 ? (uint32_t)(((1ULL << 32) + a.G - 1) / a.G) : 0;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d) * KV4_BACK);  // the keys come * 2^-72
     a.part = reinterpret_cast<float*>(workspace);
@@ -930,7 +925,7 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
         e = launch_kv4_prefill(a, d, s);
         if (e != cudaSuccess) return set_error(LLM_ERR_CUDA, cudaGetErrorString(e));
     }
-    if (d == 128) e = nt == 1 ? launch_attn<128, 1>(a, grid, s) : nt == 2 ? launch_attn<128, 2>(a, grid, s) : launch_attn<128, 4>(a, grid, s);
-    else e = nt == 1 ? launch_attn<64, 1>(a, grid, s) : nt == 2 ? launch_attn<64, 2>(a, grid, s) : launch_attn<64, 4>(a, grid, s);
+    if (d == 128) e = nt == 1 ? launch_attn<128, 1>(a, wide, grid, s) : nt == 2 ? launch_attn<128, 2>(a, wide, grid, s) : launch_attn<128, 4>(a, wide, grid, s);
+    else e = nt == 1 ? launch_attn<64, 1>(a, wide, grid, s) : nt == 2 ? launch_attn<64, 2>(a, wide, grid, s) : launch_attn<64, 4>(a, wide, grid, s);
     return e == cudaSuccess ? LLM_OK : set_error(LLM_ERR_CUDA, cudaGetErrorString(e));
 }

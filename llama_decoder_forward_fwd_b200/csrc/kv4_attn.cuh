@@ -60,11 +60,13 @@ constexpr int KV4_REST = 2;
 // that is for r < 2^32 / G, and rows of a call are fewer (the entry point checks).
 DEVI int div_g(const Kv4AttnArgs& a, int r) { return a.G == 1 ? r : (int)__umulhi((uint32_t)r, a.g_mul); }
 
-// Units of work lie on one line, more of them than 32 bits count where many rows meet many keys. A CTA's share
-// fits an int, and within it units are counted from its first one. Units of a call, at most:
+// Units of work lie on one line. Where many rows meet many keys there are more of them than 32 bits count; the
+// kernel that counts in 64 is for those calls alone (one sequence of 2100 keys: 10.4 us with it, 10.1 without). A
+// CTA's share fits an int, and within it units are counted from its first one. Units of a call, at most:
 __host__ __device__ constexpr long long kv4_most_units(int ctas) { return (long long)ctas << 29; }
-// a / b, as 32-bit numbers where they are such.
-DEVI int quotient(long long a, int b) { return a <= 0x7fffffff ? (int)a / b : (int)(a / b); }
+// ceil(a / b) for 0 <= a, 1 <= b.
+DEVI int div_up(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }
+DEVI int div_up(long long a, int b) { return (int)((a + b - 1) / b); }
 
 // The prompts' kernel. Blocks of a call, at most:
 inline long long kv4_prefill_blocks(int B, int N, int G, int few) {

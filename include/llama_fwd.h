@@ -417,7 +417,7 @@ size_t llm_kv4_page_bytes(int Hk, int d, int page_size);
  * beyond max_blocks) gets slot -1 and table entry -1, and used_out counts the pages
  * that were wanted, so used_out > n_free means that the pool ran out. N must be at
  * least the sum of n_new: tokens from row N on get neither row nor page entry.
- * No output may overlap an input other than table (LLM_ERR_BAD_ARG).
+ * No output may overlap an input other than table, or another output (LLM_ERR_BAD_ARG).
  */
 int llm_op_kv_pages(const int32_t* lens, const int32_t* n_new, int B, int page_size,
                     const int32_t* free_pages, int n_free, const int32_t* used_in, int32_t* table,
@@ -446,7 +446,9 @@ int llm_op_kv_pages(const int32_t* lens, const int32_t* n_new, int B, int page_s
  * A row whose position is outside [0, n_pos) is skipped altogether; one whose slot is
  * outside the pool gets its q_out, k_out and v_out but is not stored. Slots of one
  * call must differ: the content of one given twice is unspecified.
- * Errors: LLM_ERR_NULL_PTR, LLM_ERR_BAD_ARG (sizes, strides, 16-byte alignment),
+ * No output may overlap an input or another output, but q_out may be q itself where that is
+ * bf16 with its rows H d apart, and so k_out k and v_out v (LLM_ERR_BAD_ARG).
+ * Errors: LLM_ERR_NULL_PTR, LLM_ERR_BAD_ARG (sizes, strides, 16-byte alignment, overlaps),
  * LLM_ERR_UNSUPPORTED (d), LLM_ERR_CUDA. N == 0 is a call without work.
  */
 int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void* v, int64_t q_ld, int64_t k_ld,
@@ -474,7 +476,8 @@ int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void* v, int64_t
  * equal calls give equal bits. Masked keys do not reach a row, whatever they hold
  * (NaN and infinities included).
  * workspace: device scratch of llm_op_attention_kv4_workspace(...) bytes (0 for a bad
- * shape), 16-byte aligned, contents arbitrary; calls sharing one must not overlap in time.
+ * shape), 16-byte aligned, contents arbitrary; calls sharing one must not overlap in time. out
+ * and the workspace may not overlap an input or one another (LLM_ERR_BAD_ARG).
  * From some 1000 query rows per KV head and sequence on, part of it is room to expand the
  * prompts' cache to bf16 once: what tables filled to their width would need, or 64 MiB where
  * that passes 1 GiB. A call uses what room it is given beyond its least (that of max_new =

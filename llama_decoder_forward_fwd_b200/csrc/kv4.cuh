@@ -60,6 +60,33 @@ DEVI void kv4_expand(uint32_t w, uint32_t s2, uint32_t s2_16th, uint32_t z2, uin
     }
 }
 
+// ---- the entry points' checks ----
+struct Bytes {
+    const void* p;
+    size_t n;  // 0: nothing
+};
+inline bool overlap(const Bytes& a, const Bytes& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
+}
+// Whether b overlaps one of n rows of `row` bytes, `apart` bytes (row or more) from one to the next.
+inline bool overlap_rows(const void* rows, size_t row, long long apart, int n, const Bytes& b) {
+    if (n < 1 || !b.p || !b.n) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(rows), y = reinterpret_cast<uintptr_t>(b.p);
+    const unsigned long long i = y < x + row ? 0 : n == 1 ? 1 : (y - x - row) / apart + 1;  // the first row that ends behind b's begin
+    return i < (unsigned long long)n && x + i * apart < y + b.n;
+}
+// Whether one of the outputs overlaps an input or another output.
+template <int I, int O> bool any_overlap(const Bytes (&in)[I], const Bytes (&out)[O]) {
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (overlap(in[i], out[o])) return true;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[i], out[o])) return true;
+    }
+    return false;
+}
+
 // ---- what the model's own path uses ----
 // llm_op_kv_pages; n_new null: n_each new tokens for every sequence; held > 0: the pages taken already are
 // those of the first `held` lengths, whatever became of earlier plans (used_in and used_out null).

@@ -328,6 +328,23 @@ extern "C" int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void*
         all |= reinterpret_cast<uintptr_t>(p);
     if (all & 15) return set_error(LLM_ERR_BAD_ARG, "operands must be 16-byte aligned");
     if ((long long)H * d > (1 << 20) || N > (1 << 30)) return set_error(LLM_ERR_UNSUPPORTED, "more heads or token rows than one call takes");
+    const size_t esz = dtype == LLM_F32 ? 4 : 2, wsz = norm_dtype == LLM_F32 ? 4 : 2, hd = (size_t)H * d, kd = (size_t)Hk * d;
+    const Bytes in[] = {{q_norm, d * wsz}, {k_norm, d * wsz}, {rope_cos, (size_t)n_pos * d * 2}, {rope_sin, (size_t)n_pos * d * 2},
+                        {positions, (size_t)N * 4}, {slots, (size_t)N * 8}};
+    const Bytes out[] = {{pool, n_pages * llm_kv4_page_bytes(Hk, d, page_size)}, {q_out, N * hd * 2}, {k_out, N * kd * 2},
+                         {v_out, N * kd * 2}};
+    // the rows of q, k and v: a lane reads 16 bytes of a row and writes the same ones of an output that is the row
+    const struct {
+        const void *rows, *own;
+        int64_t ld;
+        size_t n;
+    } src[] = {{q, q_out, q_ld, hd}, {k, k_out, k_ld, kd}, {v, v_out, v_ld, kd}};
+    bool bad = any_overlap(in, out);
+    for (const auto& x : src) {
+        const bool in_place = x.own == x.rows && dtype == LLM_BF16 && (N == 1 || x.ld == (int64_t)x.n);
+        for (const auto& o : out) bad = bad || (!(in_place && o.p == x.own) && overlap_rows(x.rows, x.n * esz, x.ld * (int64_t)esz, N, o));
+    }
+    if (bad) return set_error(LLM_ERR_BAD_ARG, "an output overlaps an input or another output");
     AppendArgs a{q, k, v, q_ld, k_ld, v_ld, q_norm, k_norm, eps, rope_cos, rope_sin, n_pos, positions, slots, N, H, Hk,
                  reinterpret_cast<__nv_bfloat16*>(q_out), reinterpret_cast<__nv_bfloat16*>(k_out),
                  reinterpret_cast<__nv_bfloat16*>(v_out), reinterpret_cast<uint8_t*>(pool),

@@ -881,6 +881,10 @@ int lfw::attention_kv4(const void* q, const void* pool, int n_pages, int page_si
         images_in(workspace_bytes, images_within(all_images, d, kMostImageBytes), grid, nt, d, B, N, H / Hk, Hk);
     const Ws w = ws_layout(grid, nt, d, B, N, H / Hk, prompts, n_images);
     if (workspace_bytes < w.bytes) return set_error(LLM_ERR_BAD_ARG, "workspace too small");
+    const size_t row = (size_t)H * d * 2;
+    const Bytes in[] = {{q, N * row}, {pool, n_pages * llm_kv4_page_bytes(Hk, d, page_size)}, {table, (size_t)B * max_blocks * 4},
+                        {lens, (size_t)B * 4}, {q_start, (size_t)B * 4 + 4}}, res[] = {{out, N * row}, {workspace, w.bytes}};
+    if (any_overlap(in, res)) return set_error(LLM_ERR_BAD_ARG, "out or the workspace overlaps an input or the other");
     Kv4AttnArgs a;
     a.q = reinterpret_cast<const __nv_bfloat16*>(q);
     a.pool = reinterpret_cast<const uint8_t*>(pool);

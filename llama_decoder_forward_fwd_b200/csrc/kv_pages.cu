@@ -129,11 +129,6 @@ __global__ void __launch_bounds__(PG_THREADS) kv_pages_kernel(const PagesArgs a)
     }
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace lfw
 
@@ -154,16 +149,11 @@ extern "C" int llm_op_kv_pages(const int32_t* lens, const int32_t* n_new, int B,
         return set_error(LLM_ERR_BAD_ARG, "need B >= 1, N >= 0, n_free >= 0, max_blocks >= 1, page_size 16, 32, 64 or 128");
     // every CTA reads the inputs while others already write
     const size_t nb = (size_t)B * 4;
-    const struct {
-        const void* p;
-        size_t n;
-    } in[4] = {{lens, nb}, {n_new, nb}, {free_pages, (size_t)n_free * 4}, {used_in, used_in ? size_t(4) : size_t(0)}},
-      out[6] = {{table, nb * max_blocks}, {q_start, nb + 4},  {positions, (size_t)N * 4},
-                {slots, (size_t)N * 8},   {new_lens, nb},     {used_out, 4}};
-    for (const auto& i : in)
-        for (const auto& o : out)
-            if (i.n && o.n && overlap(i.p, i.n, o.p, o.n))
-                return set_error(LLM_ERR_BAD_ARG, "an output overlaps an input (lens, n_new, free_pages, used_in)");
+    const Bytes in[] = {{lens, nb}, {n_new, nb}, {free_pages, (size_t)n_free * 4}, {used_in, 4}};
+    const Bytes out[] = {{table, nb * max_blocks}, {q_start, nb + 4}, {positions, (size_t)N * 4},
+                         {slots, (size_t)N * 8},   {new_lens, nb},    {used_out, 4}};
+    if (any_overlap(in, out))
+        return set_error(LLM_ERR_BAD_ARG, "an output overlaps an input (lens, n_new, free_pages, used_in) or another output");
     const cudaError_t e = lfw::launch_kv_pages(lens, n_new, 0, 0, B, page_size, free_pages, n_free, used_in, table, max_blocks, q_start,
                                                positions, slots, N, new_lens, used_out, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LLM_OK : set_error(LLM_ERR_CUDA, cudaGetErrorString(e));

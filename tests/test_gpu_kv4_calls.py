@@ -39,3 +39,46 @@ def test_no_call_takes_memory(lib):
             L.llm_op_attention_kv4(*a)
         L.llm_op_synchronize()
     assert torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.parametrize("N,H,Hk,d", [(1, 8, 2, 128), (300, 5, 1, 64), (70, 4, 4, 128)])
+def test_append_in_place_and_between_rows(lib, N, H, Hk, d):
+    """q_out, k_out and v_out may be q, k and v themselves, and may lie between the rows of strided ones."""
+    import llama_decoder_forward_fwd_b200 as L
+    bf, dev, P = torch.bfloat16, "cuda", 16
+    g = torch.Generator(device=dev).manual_seed(N)
+    rand = lambda *s: torch.randn(*s, device=dev, generator=g).to(bf)
+    q, k, v, w = rand(N, H, d), rand(N, Hk, d), rand(N, Hk, d), rand(d)
+    ang = torch.rand(N + 9, d // 2, device=dev, generator=g)
+    n_pages = -(-N // P)
+    tables = torch.cos(ang), torch.sin(ang)
+    pos, slots = torch.randperm(N, device=dev, generator=g).int(), torch.randperm(n_pages * P, device=dev, generator=g)[:N]
+
+    def run(q, k, v, q_out, k_out, v_out):
+        pool = torch.zeros(n_pages, L.llm_kv4_page_bytes(Hk, d, P), dtype=torch.uint8, device=dev)
+        torch.cuda.synchronize()
+        L.llm_op_qk_norm_rope_kv4(q, k, v, pos, slots, *tables, q_out, pool, P, q_norm=w, k_norm=w, k_out=k_out, v_out=v_out)
+        L.llm_op_synchronize()
+        return q_out, k_out, v_out, pool
+    want = run(q, k, v, torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+    x, y, z = q.clone(), k.clone(), v.clone()
+    for a, b in zip(run(x, y, z, x, y, z), want):
+        assert torch.equal(a, b)
+    # two token rows far apart, with the outputs in the gap; and one wide row that holds all of a token
+    if N > 1:
+        n = (2 * H + 4 * Hk) * d
+        room = torch.empty(2, 2 * n, dtype=bf, device=dev)
+        part = lambda at, heads: room[:, at:at + heads * d].unflatten(1, (heads, d))
+        ins = part(0, H), part(H * d, Hk), part((H + Hk) * d, Hk)
+        for a, b in zip(ins, (q, k, v)):
+            a.copy_(b[:2])
+        gap, at = room[0, (H + 2 * Hk) * d:], 0
+        outs = []
+        for heads in (H, Hk, Hk):
+            outs.append(gap[at:at + 2 * heads * d].view(2, heads, d))
+            at += 2 * heads * d
+        pos, slots = pos[:2].clone(), slots[:2].clone()
+        got = run(*ins, *outs)
+        want = run(q[:2].contiguous(), k[:2].contiguous(), v[:2].contiguous(), *(torch.empty_like(t) for t in outs))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -52,3 +52,49 @@ def test_the_workspace_of_expanded_prompts_is_bounded(lib):
         last = size(2, tokens)
     for B, tokens in ((3, 131072), (16, 32768), (2, 1 << 24), (64, 1 << 20)):
         assert (64 << 20) < size(B, tokens) < (64 + 50 << 20)
+
+
+# ---------------------------------------------------------------- operands that overlap
+# Refusals only: with the overlap taken away these addresses would be read.
+MB = 1 << 20
+PAGES = dict(lens=1 * MB, n_new=2 * MB, B=4, page_size=16, free_pages=3 * MB, n_free=9, used_in=4 * MB, table=5 * MB,
+             max_blocks=8, q_start=6 * MB, positions=7 * MB, slots=8 * MB, N=10, new_lens=9 * MB, used_out=10 * MB, stream=None)
+
+
+@pytest.mark.parametrize("kw", [dict(q_start=PAGES["new_lens"] - 16), dict(used_out=PAGES["q_start"] + 16),
+                                dict(positions=PAGES["slots"] + 76), dict(table=PAGES["positions"] - 124),
+                                dict(new_lens=PAGES["table"])])
+def test_plan_refuses_outputs_that_overlap(lib, kw):
+    assert lib.llm_op_kv_pages(*(PAGES | kw).values()) == L.LLM_ERR_BAD_ARG
+    assert "overlaps" in lib.llm_last_error().decode()
+
+
+APPEND = dict(q=16 * MB, k=32 * MB, v=48 * MB, q_ld=6 * 128, k_ld=6 * 128, v_ld=6 * 128, dtype=L.LLM_BF16, q_norm=1 * MB,
+              k_norm=2 * MB, norm_dtype=L.LLM_F32, eps=1e-5, rope_cos=3 * MB, rope_sin=4 * MB, n_pos=10, positions=5 * MB,
+              slots=6 * MB, N=3, H=4, Hk=1, d=128, q_out=64 * MB, pool=80 * MB, n_pages=2, page_size=16, k_out=96 * MB,
+              v_out=112 * MB, stream=None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=APPEND["q"]),                                   # rows of other strides
+    dict(q_out=APPEND["q"], q_ld=4 * 128, dtype=L.LLM_F32),    # and of another type
+    dict(q_out=APPEND["q"] + 16, q_ld=4 * 128),
+    dict(q_out=APPEND["k"]), dict(k_out=APPEND["v"]), dict(k_out=APPEND["k"] + 2 * 6 * 128 * 2 + 240),
+    dict(q_out=APPEND["q_norm"]), dict(v_out=APPEND["rope_sin"] + 2544), dict(pool=APPEND["slots"] - 5104),
+    dict(k_out=APPEND["v_out"] + 752), dict(q_out=APPEND["pool"] + 5104), dict(pool=APPEND["v"] - 16),
+    dict(q_out=APPEND["positions"])])
+def test_append_refuses_operands_that_overlap(lib, kw):
+    assert lib.llm_op_qk_norm_rope_kv4(*(APPEND | kw).values()) == L.LLM_ERR_BAD_ARG
+    assert "overlaps" in lib.llm_last_error().decode()
+
+
+ATTEND = dict(q=16 * MB, pool=32 * MB, n_pages=4, page_size=16, table=1 * MB, max_blocks=4, lens=2 * MB, q_start=3 * MB, B=2,
+              N=2, max_new=1, H=4, Hk=2, d=128, out=48 * MB, workspace=64 * MB, workspace_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw", [dict(out=ATTEND["q"]), dict(out=ATTEND["q"] - 2032), dict(out=ATTEND["pool"] + 16),
+                                dict(out=ATTEND["lens"]), dict(workspace=ATTEND["q"] + 2032), dict(out=ATTEND["workspace"] + 4096),
+                                dict(workspace=ATTEND["table"]), dict(workspace=ATTEND["q_start"])])
+def test_attention_refuses_operands_that_overlap(lib, kw):
+    assert lib.llm_op_attention_kv4(*(ATTEND | kw).values()) == L.LLM_ERR_BAD_ARG
+    assert "overlaps" in lib.llm_last_error().decode()

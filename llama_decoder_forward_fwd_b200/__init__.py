@@ -375,6 +375,13 @@ def _bad(t, dtype, shape, dev):
     return t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous()
 
 
+def _rank(n, **operands):
+    """Raise for the first of name=tensor that has not n dimensions."""
+    for name, t in operands.items():
+        if t.dim() != n:
+            raise LlmError(LLM_ERR_BAD_ARG, f"{name} must have {n} dimensions; it has the shape {tuple(t.shape)}")
+
+
 def _pool_pages(pool, Hk, d, page_size):
     # llm_kv4_page_bytes of the sizes that the C side takes (it refuses others), without another call into it
     shape = pool.shape
@@ -392,6 +399,9 @@ def llm_op_kv_pages(lens, n_new, page_size, free_pages, used_in, table, q_start,
     """Block tables and slot maps from request lengths. lens, n_new, new_lens int32 [B]; free_pages int32 [n_free];
     used_in (or None), used_out int32 [1]; table int32 [B, max_blocks]; q_start int32 [B+1]; positions int32 [N];
     slots int64 [N]."""
+    if lens.dim() != 1 or positions.dim() != 1 or free_pages.dim() != 1 or table.dim() != 2:
+        _rank(1, lens=lens, positions=positions, free_pages=free_pages)
+        _rank(2, table=table)
     dev, B, N, n_free, blocks = _device(), lens.shape[0], positions.shape[0], free_pages.shape[0], table.shape[-1]
     bs, ns, one = (B,), (N,), (1,)
     if (_bad(lens, _I32, bs, dev) or _bad(n_new, _I32, bs, dev) or _bad(free_pages, _I32, (n_free,), dev)
@@ -425,6 +435,9 @@ def llm_op_qk_norm_rope_kv4(q, k, v, positions, slots, rope_cos, rope_sin, q_out
     """Norms of queries and keys per head, rotation, append in 4 bits. q [N,H,d], k, v [N,Hk,d], fp32 or bf16 (any
     stride between tokens); positions int32 [N]; slots int64 [N]; rope_cos, rope_sin fp32 [n_pos, d/2]; q_out bf16
     [N,H,d]; pool uint8 [n_pages, llm_kv4_page_bytes]; q_norm, k_norm [d]; k_out, v_out bf16 [N,Hk,d] or None."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or rope_cos.dim() != 2:
+        _rank(3, q=q, k=k, v=v)
+        _rank(2, rope_cos=rope_cos)
     (N, H, d), Hk, t, dev, n_pos = q.shape, k.shape[1], q.dtype, _device(), rope_cos.shape[0]
     w = q_norm if q_norm is not None else k_norm
     wt = _F32 if w is None else w.dtype
@@ -456,6 +469,9 @@ def llm_op_attention_kv4_workspace(B, N, max_new, H, Hk, d, max_blocks, page_siz
 def llm_op_attention_kv4(q, pool, page_size, Hk, table, lens, q_start, max_new, out, workspace, stream=None):
     """Attention over the 4-bit pages. q bf16 [N,H,d]; pool uint8 [n_pages, llm_kv4_page_bytes]; table int32
     [B, max_blocks]; lens int32 [B]; q_start int32 [B+1]; out bf16 [N, H*d]."""
+    if q.dim() != 3 or table.dim() != 2:
+        _rank(3, q=q)
+        _rank(2, table=table)
     (N, H, d), (B, blocks), dev = q.shape, table.shape, _device()
     if (_bad(q, _BF, (N, H, d), dev) or _bad(pool, _U8, pool.shape, dev) or _bad(table, _I32, (B, blocks), dev)
             or _bad(lens, _I32, (B,), dev) or _bad(q_start, _I32, (B + 1,), dev) or _bad(out, _BF, (N, H * d), dev)

@@ -98,3 +98,26 @@ ATTEND = dict(q=16 * MB, pool=32 * MB, n_pages=4, page_size=16, table=1 * MB, ma
 def test_attention_refuses_operands_that_overlap(lib, kw):
     assert lib.llm_op_attention_kv4(*(ATTEND | kw).values()) == L.LLM_ERR_BAD_ARG
     assert "overlaps" in lib.llm_last_error().decode()
+
+
+# ---------------------------------------------------------------- what the binding sees before any call
+def test_binding_refuses_operands_of_another_rank(lib):
+    import torch
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    f, bf = torch.zeros, lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    i64 = lambda *s: torch.zeros(*s, dtype=torch.int64)
+    pages = dict(lens=i(2), n_new=i(2), page_size=16, free_pages=i(4), used_in=i(1), table=i(2, 3), q_start=i(3), positions=i(5),
+                 slots=i64(5), new_lens=i(2), used_out=i(1))
+    append = dict(q=bf(5, 4, 128), k=bf(5, 2, 128), v=bf(5, 2, 128), positions=i(5), slots=i64(5), rope_cos=f(9, 64),
+                  rope_sin=f(9, 64), q_out=bf(5, 4, 128), pool=u8(3, 5120), page_size=16)
+    attend = dict(q=bf(5, 4, 128), pool=u8(3, 5120), page_size=16, Hk=2, table=i(2, 3), lens=i(2), q_start=i(3), max_new=5,
+                  out=bf(5, 512), workspace=u8(64))
+    for call, good, names in ((L.llm_op_kv_pages, pages, ("lens", "free_pages", "table", "positions", "n_new", "used_out")),
+                              (L.llm_op_qk_norm_rope_kv4, append, ("q", "k", "v", "rope_cos", "rope_sin", "positions", "q_out")),
+                              (L.llm_op_attention_kv4, attend, ("q", "pool", "table", "lens", "q_start", "out"))):
+        for name in names:
+            for x in (good[name].flatten() if good[name].dim() > 1 else good[name][None], good[name].sum()):
+                with pytest.raises(L.LlmError) as e:
+                    call(**(good | {name: x}))
+                assert e.value.code == L.LLM_ERR_BAD_ARG, name

@@ -87,11 +87,17 @@ extern "C" {
 
 #define LLM_FLAG_KV4           32 /* keep the KV cache in 4 bits, in pages of 64 tokens (see the paged
                                     cache below): 1.25 head_dim bytes per position and KV head, K
-                                    and V together, instead of 4 (and up to 1 GiB of workspace for
-                                    long prompts). bf16 models with head_dim 64 or 128;
+                                    and V together, instead of 4. Beside it lie one layer's keys
+                                    and values in bf16 and the attention's workspace (up to 1 GiB
+                                    for long prompts). Keys and values are rounded to bf16
+                                    before they are coded, and decode steps pass the attention's
+                                    output on in bf16, without the remainder that they keep
+                                    with the bf16 cache. bf16 models with head_dim 64 or 128;
                                     LLM_FLAG_FUSED_DECODE has no effect beside it,
                                     llm_kv_cache_view and llm_kv_cache_set_lens return
-                                    LLM_ERR_UNSUPPORTED (the cache is filled by the model alone) */
+                                    LLM_ERR_UNSUPPORTED (the cache is filled by the model alone),
+                                    and so do calls of more rows over max_seq_len positions than
+                                    llm_op_attention_kv4 takes */
 
 /* ---- kernel kinds reported by llm_kernel_times ------------------------- */
 #define LLM_K_EMBED    0   /* embedding lookup / hidden-state load */
@@ -429,7 +435,8 @@ int llm_op_kv_pages(const int32_t* lens, const int32_t* n_new, int B, int page_s
  * of every query and key head (q_norm, k_norm: device [d] of norm_dtype, NULL: none;
  * y = x w / sqrt(mean x^2 + eps)), rotation of the pairs (2i, 2i+1) at the token's
  * position (llama3.np "RoPE #1", "RoPE #2"), and the append of the rotated keys and
- * the values to the 4-bit cache.
+ * the values to the 4-bit cache. Checkpoints that rotate the pairs (i, i + d/2) need the rows of
+ * their projections, and their norm weights, permuted to (2i, 2i+1).
  *   q, k, v   device [N] rows of [H][d], [Hk][d], [Hk][d], dtype LLM_F32 or
  *             LLM_BF16; rows q_ld, k_ld, v_ld elements apart (multiples of 16
  *             bytes; they may be parts of one projection's output)
@@ -470,11 +477,11 @@ int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void* v, int64_t
  *   q_start   device int32 [B+1], not decreasing, within [0, N]
  *   max_new   host: at least the largest q_start[b+1] - q_start[b]; the kernel is chosen
  *             by it (a smaller value costs time, not results)
- * Scale 1/sqrt(d); query head h reads KV head h / (H/Hk). A row that sees no key gives
- * 0; rows of out from q_start[B] on are left as they were. The softmax weights enter the
- * second product rounded to bf16, sums are fp32, and the order of every sum is fixed:
- * equal calls give equal bits. Masked keys do not reach a row, whatever they hold
- * (NaN and infinities included).
+ * Scale 1/sqrt(d); query head h reads KV head h / (H/Hk). A row that sees no key, or only
+ * scores of -infinity, gives 0, and one that sees a score of NaN or +infinity NaN; rows of out
+ * from q_start[B] on are left as they were. The softmax weights enter the second product
+ * rounded to bf16, sums are fp32, and the order of every sum is fixed: equal calls give equal
+ * bits. Masked keys do not reach a row, whatever they hold (NaN and infinities included).
  * workspace: device scratch of llm_op_attention_kv4_workspace(...) bytes (0 for a bad
  * shape), 16-byte aligned, contents arbitrary; calls sharing one must not overlap in time. out
  * and the workspace may not overlap an input or one another (LLM_ERR_BAD_ARG).

@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the forward pass runs in the library's
 CUDA kernels. The functions below carry the C names; ``Model`` bundles a model
 handle with the tensors whose device pointers it holds. There is no fallback:
-if the shared library is missing, ``load()`` raises.
+if the shared library is missing, ``load()`` raises. Operations run on the stream that
+they are given, ``stream=None`` being the legacy default stream and not torch's current
+one: inside ``torch.cuda.stream(s)``, pass ``stream=s``.
 """
 from __future__ import annotations
 

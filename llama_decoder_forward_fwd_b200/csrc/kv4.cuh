@@ -60,6 +60,13 @@ DEVI void kv4_expand(uint32_t w, uint32_t s2, uint32_t s2_16th, uint32_t z2, uin
     }
 }
 
+// A maximum that a NaN does not drop out of.
+DEVI float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // ---- the entry points' checks ----
 struct Bytes {
     const void* p;

@@ -11,9 +11,10 @@
 // reads back as NaN instead of passing for finite values.
 //
 // The keys' norm and rotation run in fp64. A code is a rounding decision with steps of a
-// fifteenth of the range: in fp32 the order of a sum would decide a code near a border,
-// and the cache's contents would depend on the kernel that wrote them. The queries,
-// rounded to bf16 next, take fp32.
+// fifteenth of the range: in fp32 the order of a sum would decide a code near a border, and
+// what a call stores would depend on how its kernel sums. The queries, rounded to bf16 next,
+// take fp32. (LLM_FLAG_KV4's own path does not come through here: its keys are rotated in fp32
+// by the projection's epilogue and rounded to bf16, and kv4_store_kernel codes those.)
 //
 // Every input element is read once, in 16-byte loads; a lane holds 8 consecutive values, so a
 // head row is 16 lanes at d = 128 (8 at 64), a group of 32 is 4 lanes, and the code word of a
@@ -102,15 +103,10 @@ DEVI void norm_rotate(A (&y)[VPL], const float (&x)[VPL], bool norm, const float
     }
 }
 
-// Minimum and maximum that a NaN does not drop out of.
+// A minimum that a NaN does not drop out of.
 DEVI float min_nan(float a, float b) {
     float d;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-DEVI float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 

@@ -70,11 +70,6 @@ struct Seq {
 
 DEVI uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
-DEVI float ex2a(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // v * inv, and NaN for an infinite v: the mark of a row that sees a value that is not finite.
 DEVI float scaled(float v, float inv) { return fmaf(v, 0.f, v * inv); }
 // As mma_bf16_16816, but free to move: the expansions between the products fill its latency.
@@ -468,7 +463,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
 #pragma unroll
                                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                                     const float mn = fmaxf(m[nt][e], mx * a.scale_log2);
-                                    const float al = m[nt][e] == mn ? 1.f : ex2a(m[nt][e] - mn);
+                                    const float al = m[nt][e] == mn ? 1.f : ex2(m[nt][e] - mn);
                                     m[nt][e] = mn;
                                     l[nt][e] *= al;
                                     x[nt][e] = fmaf(sc[nt][e], a.scale_log2, -mn);
@@ -482,10 +477,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const float p0f = ex2a(x[nt][0]), p1f = ex2a(x[nt][1]), p2f = ex2a(x[nt][2]), p3f = ex2a(x[nt][3]);
+                            const float p0f = ex2(x[nt][0]), p1f = ex2(x[nt][1]), p2f = ex2(x[nt][2]), p3f = ex2(x[nt][3]);
                             l[nt][0] += p0f + p2f;
                             l[nt][1] += p1f + p3f;
-                            // P enters the product in bf16 (2^-9 of each weight, over sums that the
+                            // P enters the product in bf16 (2^-8 of each weight at most, over sums that the
                             // output rounds to bf16 as well); the sum l keeps the full weights
                             pf[nt][0] = movm_t(pack_bf16x2(p0f, p1f));
                             pf[nt][1] = movm_t(pack_bf16x2(p2f, p3f));
@@ -629,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) kv4_attn_kernel(con
             float mx = ml.x;
 #pragma unroll
             for (int o = 1; o < WL; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float wgt = ex2a(ml.x - mx);
+            const float wgt = ex2(ml.x - mx);
             float lsum = wgt * ml.y;
 #pragma unroll
             for (int o = 1; o < WL; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
@@ -700,7 +695,7 @@ template <int D, int NT> __global__ void __launch_bounds__(256) kv4_attn_join_ke
 #pragma unroll 8
         for (int i = q; i < it.x; i += 4) {
             const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(i) * R * 2 + rl * 2);
-            const float wgt = ex2a(ml.x - mx);
+            const float wgt = ex2(ml.x - mx);
             lsum = fmaf(wgt, ml.y, lsum);
             const float* f = a.part + slot(i) * R * D + rl * D + lane * VPL;
 #pragma unroll

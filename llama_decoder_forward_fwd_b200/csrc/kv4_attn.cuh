@@ -56,6 +56,13 @@ struct Kv4AttnArgs {
 
 constexpr int KV4_REST = 2;
 
+// 2^x by the special-function unit, subnormals flushed: a few ulp, far below the bf16 rounding that weights get; 2^-inf = 0.
+DEVI float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // r / G for 0 <= r < 2^31: g_mul is ceil(2^32 / G), exact while r * (g_mul G - 2^32) < 2^32,
 // that is for r < 2^32 / G, and rows of a call are fewer (the entry point checks).
 DEVI int div_g(const Kv4AttnArgs& a, int r) { return a.G == 1 ? r : (int)__umulhi((uint32_t)r, a.g_mul); }

@@ -1,18 +1,19 @@
 // Attention over the 4-bit paged cache for prompts: sequences with many new tokens, whose
 // products belong on the 5th-generation tensor cores.
 //
-// A work item is 128 query rows (token, head of the KV head's group; 256 in the second variant) of one sequence and
-// KV head, as in the bf16 prefill kernel: S = Q K^T and O += P V by tcgen05 with S, P and O
-// in tensor memory, two softmax threads per row, O rescaled only when a row's maximum grows
-// by more than 2^8. What differs is where K and V come from, in two variants:
+// A work item is a block of query rows (token, head of the KV head's group) of one sequence and KV head, as in the
+// bf16 prefill kernel: S = Q K^T and O += P V by tcgen05 with S, P and O in tensor memory, O rescaled only
+// when a row's maximum grows by more than 2^8. What differs is where K and V come from, in two variants:
 //
 // - With few row blocks a sequence, four warps read the codes from the pages (the next tile's into
 //   registers while one is worked on), expand them and store the bf16 tiles in the 128-byte
 //   swizzle that the tensor cores read: some 1800 instructions a 128-key tile next to the
-//   softmax's 16,000 scores, repeated by every row block.
+//   softmax's 16,000 scores, repeated by every block of 128 rows. Two softmax threads a row.
 // - With many, a kernel before expands each sequence once, into tiles laid out like that, and one thread
 //   copies a tile in one bulk copy. That moves 4 d bytes per key and KV head out and back through L2
-//   and takes a workspace of the size of the prompts' bf16 cache. 256 rows share a tile.
+//   and takes a workspace of the size of the prompts' bf16 cache. A block has 256 rows, which share a tile, and
+//   one softmax thread a row. Prompts for whose tiles the workspace has no room take the first variant, in a
+//   second turn.
 //
 // Two orders inside 8 values: a code word expands to the pairs (0, 4), (1, 5), (2, 6),
 // (3, 7), and is stored so. Q is staged in the same order, which the contraction over d
@@ -53,17 +54,7 @@ template <int D> constexpr int kp_tile() { return D / 64 * KP_HALF; }
 template <int D> constexpr int kq_smem() { return 6 * kp_tile<D>() + 256 + 1024; }
 template <int D> constexpr int kp_smem() { return 1024 + 5 * kp_tile<D>() + 256 + 2 * KP_ROWS * 4; }
 
-DEVI float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Maxima that a NaN does not drop out of.
-DEVI float max2(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
+// A maximum that a NaN does not drop out of.
 DEVI float max3(float a, float b, float c) {
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -709,7 +700,7 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
                 float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int i = 4; i < 64; i += 2) mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], s[i], s[i + 1]);
-                const float mine = max3(mx4[0], mx4[1], max2(mx4[2], mx4[3])) * sl2;
+                const float mine = max3(mx4[0], mx4[1], max_nan(mx4[2], mx4[3])) * sl2;
                 red_max[sb][half][r] = mine;
                 named_bar_sync(1 + q4, 64);
                 const float m_new = max3(m_used, mine, red_max[sb][half ^ 1][r]);
@@ -832,7 +823,8 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
 // Tried: S by halves of the keys, so that half of it need not wait (N = 64 takes the tensor cores as long
 // as 128: 212 us against 185); masks written into S instead of the registers (184 against 180);
 // 0, 3/8, 1/2 and 5/8 of the exponentials on the FMA pipe (191, 188, 187, 193 against 184 with 1/4); two
-// threads per row, 16 softmax warps at 96 registers (192 against 180); Q staged by the softmax warps (182 against 180).
+// threads per row, 16 softmax warps at 96 registers (192 against 180); Q of all items staged by the softmax warps
+// (182 against 180; of the first item alone, which nothing else could wait for, 176.4 against 177.2).
 template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_kernel(const Kv4AttnArgs a) {
     constexpr int TILE = kp_tile<D>();
     extern __shared__ uint8_t smem_raw[];
@@ -1051,12 +1043,12 @@ template <int D> __global__ void __launch_bounds__(KQ_THREADS, 1) kv4_expanded_k
                 }
                 float mx[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = max2(f(e), f(4 + e));
+                for (int e = 0; e < 4; ++e) mx[e] = max_nan(f(e), f(4 + e));
 #pragma unroll
                 for (int i = 8; i < 128; i += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], f(i + e), f(i + 4 + e));
-                const float m_new = max2(m_used, max3(mx[0], mx[1], max2(mx[2], mx[3])) * sl2);
+                const float m_new = max_nan(m_used, max3(mx[0], mx[1], max_nan(mx[2], mx[3])) * sl2);
                 const bool need = !(m_new <= m_used + KP_RESCALE_LOG2);  // false while the row has seen no key; true for NaN
                 if (j > 0 && __any_sync(0xffffffffu, need)) {
                     // P V of the tile before is complete: the scores were issued after it

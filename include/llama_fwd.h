@@ -493,8 +493,8 @@ int llm_op_qk_norm_rope_kv4(const void* q, const void* k, const void* v, int64_t
  * Errors: as above, and LLM_ERR_UNSUPPORTED for more than one call takes, which goes by the
  * tables' width and not by the lengths: N (H/Hk)^2 from 2^31 on, or (N H / 8 + B Hk)
  * ceil(max_blocks page_size / 32) above 2^29 per SM (2^36 on a B200: 2M new tokens of 32 heads
- * over tables of 128k tokens pass), or some 2^31 pairs of 128 query rows of a KV head and 128
- * keys. A device wait that ran out shows in llm_op_synchronize.
+ * over tables of 128k tokens pass), or 2^31 pairs of 128 query rows and 128 keys over all KV
+ * heads. A device wait that ran out shows in llm_op_synchronize.
  */
 size_t llm_op_attention_kv4_workspace(int B, int N, int max_new, int H, int Hk, int d, int max_blocks,
                                       int page_size);

@@ -847,10 +847,10 @@ extern "C" int llm_op_attention_kv4(const void* q, const void* pool, int n_pages
 }
 
 int lfw::kv4_check_size(int B, int N, int H, int Hk, int max_blocks, int page_size) {
-    // a row is divided by G as 32-bit fixed point; units: see kv4_most_units; tiles of row blocks are an int
+    // a row is divided by G as 32-bit fixed point; units: see kv4_most_units; the prompts' tiles are counted in 32 bits
     const long long G = H / Hk, chunks = (long long)N * G / 8 + B, keys = (long long)max_blocks * page_size;
     if ((long long)N * G * G >= (1LL << 31) || chunks * Hk > kv4_most_units(current_num_sms()) / ((keys + KA_KEYS - 1) / KA_KEYS) ||
-        kv4_prefill_blocks(B, N, (int)G, kFewRows) >= (1LL << 31) / (keys / 128 + 4))
+        kv4_prefill_blocks(B, N, (int)G, kFewRows) * Hk >= (1LL << 31) / (keys / 128 + 4))
         return set_error(LLM_ERR_UNSUPPORTED, "more query rows over tables this wide than one call takes");
     return LLM_OK;
 }

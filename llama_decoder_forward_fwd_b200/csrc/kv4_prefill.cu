@@ -300,27 +300,19 @@ __global__ void __launch_bounds__(KP_LIST) kv4_blocks_kernel(const Kv4AttnArgs a
     }
     // The CTAs' shares: the item in which one begins says where. A share that would begin in an
     // item's fixed cost begins with its first tile.
-    auto cut = [&](auto heads) {
-        using I = decltype(heads);
-        const I units = tiles * heads;
-        const int per = max(KP_SHARE, div_up(units, sms)), ctas = div_up(units, per);
-        if (tid == 0) {
-            a.counts[0] = ctas;
-            a.counts[1] = listed;
-            a.starts[ctas] = make_int4(blocks, 0, 0, 0);
+    const int units = tiles * a.Hk, per = max(KP_SHARE, div_up(units, sms)), ctas = div_up(units, per);
+    if (tid == 0) {
+        a.counts[0] = ctas;
+        a.counts[1] = listed;
+        a.starts[ctas] = make_int4(blocks, 0, 0, 0);
+    }
+    for (int i = tid; i < blocks; i += KP_LIST) {
+        const int len = a.blocks[i].nkt + item, lo = a.blocks[i].start * a.Hk, hi = lo + len * a.Hk;
+        for (int c = div_up(lo, per); c < ctas && c * per < hi; ++c) {
+            const int off = c * per - lo, kvh = off / len;
+            a.starts[c] = make_int4(i, kvh, max(0, off - kvh * len - item), 0);
         }
-        for (int i = tid; i < blocks; i += KP_LIST) {
-            const int len = a.blocks[i].nkt + item;
-            const I lo = a.blocks[i].start * heads, hi = lo + len * heads;
-            for (int c = div_up(lo, per); c < ctas && (I)c * per < hi; ++c) {
-                const I off = (I)c * per - lo;
-                const int kvh = (int)(off / len);
-                a.starts[c] = make_int4(i, kvh, max(0, (int)(off - (I)kvh * len) - item), 0);
-            }
-        }
-    };
-    if ((long long)tiles * a.Hk < 1LL << 30) cut(a.Hk);
-    else cut((long long)a.Hk);
+    }
 }
 
 // Expand the listed sequences: a CTA writes one K or V tile as the tensor cores read it (rows of 64

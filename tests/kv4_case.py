@@ -38,7 +38,7 @@ class Case:
         self.n_pages = sum(need) + 2
         self.blocks = blocks or max(need) + 1
         ids, at = r.permutation(self.n_pages), 0
-        self.table = np.full((len(lens), self.blocks), -1)
+        self.table = np.full((len(lens), self.blocks), -1, np.int32)
         pool = K.Pool(self.n_pages, Hk, d, P, fill=0xFF)  # NaN pairs wherever nothing is stored
         self.kv = []
         for b, l in enumerate(lens):
@@ -65,7 +65,7 @@ class Case:
         mx = max(self.new) if max_new is None else max_new
         ask = L.llm_op_attention_kv4_workspace(len(self.lens), self.N + self.pad, mx, self.H, self.Hk, self.d, self.blocks, self.P)
         ws = torch.full((ask if room is None else room,), 255, dtype=torch.uint8, device="cuda")
-        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(torch.int32).cuda()
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
         out = torch.full((self.N + self.pad, self.H * self.d), -7.0, dtype=torch.bfloat16, device="cuda")
         return [self.q.cuda(), torch.from_numpy(self.pool).cuda(), self.P, self.Hk, dev(self.table), dev(self.lens),
                 dev(self.q_start), mx, out, ws]
@@ -89,6 +89,7 @@ class Case:
         if drop is not None:
             seen[:, drop] = False
         out, bound = np.zeros((n, self.H, self.d)), np.zeros((n, self.H, self.d))
+        odd, v = ~np.isfinite(v), np.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0)
         for h in range(self.H):
             with np.errstate(all="ignore"):
                 s = np.where(seen, q[:, h] @ k[:, h // G].T / np.sqrt(self.d), -np.inf)
@@ -96,7 +97,8 @@ class Case:
                 w = np.where(seen, np.exp(s - np.where(m == -np.inf, 0, m)), 0.0)
                 w /= np.where(m == -np.inf, 1, w.sum(1, keepdims=True))
                 out[:, h] = w @ v[:, h // G]
-                bound[:, h] = 2.0**-8 * np.abs(out[:, h]) + (2.0**-8 + 2.0**-11) * (w @ np.abs(v[:, h // G]))
+                out[:, h][seen.astype(np.float64) @ odd[:, h // G] > 0] = np.nan  # of the rows that see it
+                bound[:, h] = 2.0**-8 * np.abs(np.nan_to_num(out[:, h])) + (2.0**-8 + 2.0**-11) * (w @ np.abs(v[:, h // G]))
         return out, bound
 
     def check(self, got, rows=None):

@@ -70,7 +70,14 @@ def test_wide_page_tables_do_not_change_the_kernel(lib, d, P):
 def test_a_workspace_with_room_for_some_of_the_prompts(lib, d, P, lens, new):
     """From none of the expanded tiles to all of them: what has no room is expanded row block by row block."""
     import llama_decoder_forward_fwd_b200 as L
-    case = Case(lens, new, 8, 2, d, P, 10, make=marked(2, d, lens), q_scale=0.1, pad=1)
+    mark = marked(2, d, lens)
+
+    def make(b, which, r):
+        x = mark(b, which, r)
+        if which and b % 2:
+            x[-7, 1] = np.nan  # of a sequence that turns from the prompts' kernels to the other
+        return x
+    case = Case(lens, new, 8, 2, d, P, 10, make=make, q_scale=0.1, pad=1)
     shape = (len(lens), case.N + 1)
     full = L.llm_op_attention_kv4_workspace(*shape, MANY, 8, 2, d, case.blocks, P)
     least = L.llm_op_attention_kv4_workspace(*shape, 200, 8, 2, d, case.blocks, P)
@@ -83,3 +90,38 @@ def test_a_workspace_with_room_for_some_of_the_prompts(lib, d, P, lens, new):
     with pytest.raises(L.LlmError) as e:
         case.run(L, MANY, room=least - 1)
     assert e.value.code == L.LLM_ERR_BAD_ARG
+
+
+# B, new tokens of most, prompts among them, H, Hk, d, promised new tokens, pages a table is wide
+@pytest.mark.parametrize("B,n,prompts,H,Hk,d,mx,blocks", [
+    (1300, 1, [], 8, 2, 128, None, 4), (700, 3, [], 8, 1, 64, None, 4), (1300, 1, [0, 5, 700, 1299], 8, 2, 128, None, 4),
+    (1300, 1, [0, 5, 700, 1023, 1024, 1299], 8, 2, 64, MANY, 4),
+    (8, 3, [], 32, 8, 128, None, 1 << 23), (40, 1, [], 32, 8, 64, None, 1 << 21), (600, 1, [], 32, 8, 128, None, 1 << 17),
+    (600, 8, [], 32, 8, 64, None, 1 << 16)])
+def test_many_sequences_and_tables_that_want_64_bit_counts(lib, B, n, prompts, H, Hk, d, mx, blocks):
+    """More sequences than a warp, a CTA and two of them look at in one go; and the schedule in 64 bits, which the tables'
+    width alone asks for."""
+    import llama_decoder_forward_fwd_b200 as L
+    r = np.random.RandomState(B)
+    P = 128 if blocks > 4 else 32
+    lens = [int(x) for x in r.randint(1, 60, B)]
+    new = [min(l, int(r.randint(0, n + 1)) if n > 1 else n) for l in lens]
+    for b in prompts:
+        lens[b], new[b] = 90 + b % 30, 60 + b % 30
+    if blocks > 4:
+        assert (sum(new) * H // Hk // 8 + B) * Hk * blocks * P // 32 >= 2**31
+    case = Case(lens, new, H, Hk, d, P, 11, make=marked(Hk, d, lens), q_scale=0.1, blocks=blocks, pad=1)
+    case.check(case.run(L, mx))
+
+
+@pytest.mark.parametrize("mx", [None, 60, MANY])
+def test_sequences_that_share_pages(lib, mx):
+    """Three sequences whose tables begin with the same pages."""
+    import llama_decoder_forward_fwd_b200 as L
+    lens, new = [200, 200, 200], [2, 40, 1]
+    case = Case(lens, new, 8, 2, 128, 32, 12, pad=1)
+    case.table[1:, :5] = case.table[0, :5]
+    for b in (1, 2):
+        for which in (0, 1):
+            case.kv[b][which][:160] = case.kv[0][which][:160]
+    case.check(case.run(L, mx))

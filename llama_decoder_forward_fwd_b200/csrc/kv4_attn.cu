@@ -29,11 +29,11 @@
 //     evenly over all warps of the grid, wherever items begin or end: ragged lengths
 //     and short items cost no balance. An item's parts in one CTA are joined through
 //     shared memory, those of several CTAs by the second kernel, in a fixed order.
-// Measured (32 query heads, 8 KV heads, d = 128, one new token): 32 sequences of 8k to 16k keys
-// 109 us, 4.9 TB/s, 75% of the copy bandwidth (with the expansion and the products skipped
-// 89 us: the rest is their instructions, 690 per 32 keys of which 290 are the expansion's);
-// 16 of 4k to 8k 38 us; one of 2100 keys 10 us, of which a launch and the chain lengths ->
-// table -> codes -> join are 8.
+// Measured (32 query heads, 8 KV heads, d = 128, one new token; a few hundred calls back to back): 32 sequences of
+// 8k to 16k keys 110 us, 4.9 TB/s, 75% of the copy bandwidth (119-123 us, 67-69%, in loops of a second, which the power
+// cap takes from 1965 to 1800 MHz; with the expansion and the products skipped 89 us: the rest is their
+// instructions, 690 per 32 keys of which 290 are the expansion's); 16 of 4k to 8k 38 us; one of 2100 keys 10 us,
+// of which a launch and the chain lengths -> table -> codes -> join are 8.
 #include "../../include/llama_fwd.h"
 #include "kernels.cuh"
 #include "kv4_attn.cuh"

@@ -20,9 +20,9 @@
 // does not notice; O's columns come in it and are written out straight. Expanded before, they are put in
 // plain order, so that Q's rows can be copied.
 //
-// Measured: 134 GFLOP of prompts over a cached context 176 us, 760 TFLOP/s, 10 us of it the expansion
-// before; 252 us with the expanding warps in the kernel, which share the issue slots with the
-// softmax (a 128-key tile takes 1.8 us so).
+// Measured: 134 GFLOP of prompts over a cached context 177 us in short runs, 760 TFLOP/s, 10 us of it the
+// expansion before (185-190 us, 707-725 TFLOP/s, in loops of a second under the power cap); 252 us with the expanding
+// warps in the kernel, which share the issue slots with the softmax (a 128-key tile takes 1.8 us so).
 //
 // A small kernel before lists the row blocks. Their tiles, for each KV head, form one line that
 // is cut evenly over the SMs (one CTA each): neither ragged prompts nor few rows over a long
@@ -808,7 +808,7 @@ template <int D> __global__ void __launch_bounds__(KP_THREADS, 1) kv4_prefill_ke
 // that P lies over S, and S of a block's next tile waits for its P V. A thread has a row: nothing is
 // exchanged, and a tile of K and V serves twice the rows that the kernel above has.
 //
-// What bounds it (134 GFLOP, 176 us): the chain of a block's tile. At 1.7 GHz of 3500 clocks for two
+// What bounds it (134 GFLOP, 177 us): the chain of a block's tile. At 1.7 GHz of 3500 clocks for two
 // blocks' tiles the softmax takes 1900 (reading and maximum 600, exponentials 1200), P V behind the
 // second half of P 480, S 950; the tensor cores alone would take 2048. Some 11000 clocks of an item's
 // 70000 go by at its end, half of them while Q is staged.

@@ -13,8 +13,9 @@
 // The keys' norm and rotation run in fp64. A code is a rounding decision with steps of a
 // fifteenth of the range: in fp32 the order of a sum would decide a code near a border, and
 // what a call stores would depend on how its kernel sums. The queries, rounded to bf16 next,
-// take fp32. (LLM_FLAG_KV4's own path does not come through here: its keys are rotated in fp32
-// by the projection's epilogue and rounded to bf16, and kv4_store_kernel codes those.)
+// take fp32, with a second sum for rows whose squares pass its range. (LLM_FLAG_KV4's own path
+// does not come through here: its keys are rotated in fp32 by the projection's epilogue and
+// rounded to bf16, and kv4_store_kernel codes those.)
 //
 // Every input element is read once, in 16-byte loads; a lane holds 8 consecutive values, so a
 // head row is 16 lanes at d = 128 (8 at 64), a group of 32 is 4 lanes, and the code word of a
@@ -91,7 +92,15 @@ DEVI void norm_rotate(A (&y)[VPL], const float (&x)[VPL], bool norm, const float
         for (int i = 0; i < VPL; ++i) ss += y[i] * y[i];
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(row, ss, o);
-        const A r = inv_sqrt(ss * (A)(1.0 / (LPR * VPL)) + eps);
+        A r = inv_sqrt(ss * (A)(1.0 / (LPR * VPL)) + eps);
+        if (sizeof(A) == 4 && ss > FLT_MAX) {  // squares beyond fp32: the same of x 2^-70 (the row's lanes agree)
+            ss = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) ss += (y[i] * (A)0x1p-70) * (y[i] * (A)0x1p-70);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(row, ss, o);
+            r = (A)0x1p-70 * inv_sqrt(ss * (A)(1.0 / (LPR * VPL)) + eps * (A)0x1p-140);
+        }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) y[i] = y[i] * r * (A)w[i];
     }
